@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a16.so")
 HEADERS = ["w4a16_layout.h", "w4a16_device.h", "w4a16_internal.h", "w4a16_epilogue.h",
-           "w4a8_internal.h", "w4a8_device.h", "mx_internal.h"]
+           "w4a8_internal.h", "w4a8_device.h", "mx_internal.h", "fp8_internal.h",
+           "rowquant_internal.h"]
 
 COMMON = [
     "--offload-arch=gfx950",
@@ -51,6 +52,13 @@ UNITS = [
     ("mx_prep.hip", []),
     ("mx_gemm.hip", ["-DMXFP4_TU_BF16=0"]),
     ("mx_gemm.hip", ["-DMXFP4_TU_BF16=1"]),
+    ("fp8_api.cpp", []),
+    ("fp8_prep.hip", []),
+    ("fp8_gemm.hip", ["-DFP8_TU_BF16=0"]),
+    ("fp8_gemm.hip", ["-DFP8_TU_BF16=1"]),
+    ("rowquant_api.cpp", []),
+    ("rowquant.hip", ["-DROWQUANT_TU_BF16=0"]),
+    ("rowquant.hip", ["-DROWQUANT_TU_BF16=1"]),
 ]
 
 

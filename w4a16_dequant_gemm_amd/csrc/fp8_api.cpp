@@ -1,0 +1,170 @@
+// fp8_api.cpp -- the extern "C" entry points declared in include/fp8.h:
+// host-side validation (always before any HIP call), the kernel plan and the
+// launches.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "../../include/fp8.h"
+#include "fp8_internal.h"
+
+namespace fp8 {
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 24;
+constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxExperts = 65535;
+constexpr uint32_t kPlanBits = FP8_PLAN_MASK | (0xFFu << W4A16_PLAN_PARAM_SHIFT);
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
+
+constexpr int kDefaultCUs = 256;
+constexpr int kMaxDevices = 64;
+
+// Compute units of the current device, read once per device.
+int num_cus() {
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return kDefaultCUs;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+        n <= 0)
+        n = kDefaultCUs;
+    cache[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+w4a16_status_t check_weights(int64_t E, int64_t K, int64_t N) {
+    if (E < 1 || E > kMaxExperts || K < 1 || N < 1 || K >= kMaxDim || N >= kMaxDim)
+        return W4A16_ERR_INVALID_ARG;
+    if (K % 16 != 0) return W4A16_ERR_UNSUPPORTED;
+    if ((double)E * (double)K * (double)N >= (double)((int64_t)1 << 42))
+        return W4A16_ERR_INVALID_ARG;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int cus) {
+    Plan p{};
+    (void)N; (void)K; (void)cus;
+    const uint32_t hint = flags & FP8_PLAN_MASK;
+    const int param = (int)((flags >> W4A16_PLAN_PARAM_SHIFT) & 0xFFu);
+    const int64_t per = E ? (M + E - 1) / E : M;   // rows an expert has, on average
+    p.variant = STREAM;
+    p.cfg = hint == FP8_PLAN_STREAM && (param == 1 || param == 2) ? param : per <= 16 ? 1 : 2;
+    p.bn = 16;
+    p.bm = 16 * p.cfg;
+    p.splits = 1;
+    return p;
+}
+
+namespace {
+
+GemmArgs make_args(const uint8_t* xq, const float* xs, const void* packed, const int32_t* offsets,
+                   const int32_t* rows, void* Y, int64_t M, int64_t T, const Layout& L,
+                   const Plan& p, void* workspace) {
+    GemmArgs a{};
+    a.xq = xq;
+    a.xs = xs;
+    a.blob = (const uint8_t*)packed;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.Y = Y;
+    a.cnt = (uint32_t*)workspace;
+    a.part = workspace ? (float*)((uint8_t*)workspace + kCounterBytes) : nullptr;
+    a.M = M;
+    a.T = T;
+    a.N = (int)L.N;
+    a.K = (int)L.K;
+    a.KB = (int)L.KB;
+    a.NB = (int)L.NB;
+    a.E = (int)L.E;
+    a.splits = p.splits;
+    if (p.bn > 0) {
+        a.nbn = (int)((L.N + p.bn - 1) / p.bn);
+        a.nbm = (int)(p.tiles / a.nbn);
+    }
+    a.s_off = L.s_off;
+    a.z_off = L.z_off;
+    return a;
+}
+
+}  // namespace
+
+}  // namespace fp8
+
+using namespace fp8;
+
+extern "C" {
+
+size_t fp8_packed_bytes(int64_t E, int64_t K, int64_t N) {
+    if (check_weights(E, K, N) != W4A16_OK) return 0;
+    return make_layout(E, K, N).total;
+}
+
+w4a16_status_t fp8_repack(const uint8_t* w, const float* ws, int64_t E, int64_t K, int64_t N,
+                          void* packed, size_t packed_bytes, void* stream) {
+    const w4a16_status_t st = check_weights(E, K, N);
+    if (st != W4A16_OK) return st;
+    if (!w || !ws || !packed || !aligned16(w) || !aligned16(ws) || !aligned16(packed))
+        return W4A16_ERR_INVALID_ARG;
+    const Layout L = make_layout(E, K, N);
+    if (packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
+    return from_hip(launch_repack(w, ws, L, packed, (hipStream_t)stream));
+}
+
+size_t fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, uint32_t flags) {
+    if ((flags & ~(FP8_BF16 | kPlanBits)) || M < 1 || M >= kMaxRows ||
+        check_weights(1, K, N) != W4A16_OK)
+        return 0;
+    return make_plan(M, N, K, 0, flags, num_cus()).workspace;
+}
+
+w4a16_status_t fp8_gemm(const uint8_t* xq, const float* xs, const void* packed,
+                        size_t packed_bytes, void* Y, int64_t M, int64_t N, int64_t K,
+                        uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+    if (flags & ~(FP8_BF16 | kPlanBits)) return W4A16_ERR_INVALID_ARG;
+    if (M < 0 || M >= kMaxRows) return W4A16_ERR_INVALID_ARG;
+    const w4a16_status_t st = check_weights(1, K, N);
+    if (st != W4A16_OK) return st;
+    const Layout L = make_layout(1, K, N);
+    if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    if (!xq || !xs || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(Y))
+        return W4A16_ERR_INVALID_ARG;
+    const Plan p = make_plan(M, N, K, 0, flags, num_cus());
+    if (p.workspace > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.workspace))
+        return W4A16_ERR_WORKSPACE;
+    const GemmArgs a = make_args(xq, xs, packed, nullptr, nullptr, Y, M, M, L, p, workspace);
+    hipStream_t s = (hipStream_t)stream;
+    return from_hip((flags & FP8_BF16) ? launch_gemm_bf16(a, p, s) : launch_gemm_f16(a, p, s));
+}
+
+w4a16_status_t fp8_grouped_gemm(const uint8_t* xq, const float* xs, const void* packed,
+                                size_t packed_bytes, const int32_t* offsets, const int32_t* rows,
+                                void* Y, int64_t R, int64_t T, int64_t E, int64_t N, int64_t K,
+                                uint32_t flags, void* stream) {
+    if (flags & ~(FP8_BF16 | kPlanBits)) return W4A16_ERR_INVALID_ARG;
+    if (R < 0 || R >= kMaxRows || T < 0 || T >= kMaxRows) return W4A16_ERR_INVALID_ARG;
+    if (rows ? (T < 1 && R > 0) : T < R) return W4A16_ERR_INVALID_ARG;
+    const w4a16_status_t st = check_weights(E, K, N);
+    if (st != W4A16_OK) return st;
+    const Layout L = make_layout(E, K, N);
+    if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
+    if (R == 0) return W4A16_OK;
+    if (!xq || !xs || !offsets || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(offsets) ||
+        !aligned16(rows) || !aligned16(Y))
+        return W4A16_ERR_INVALID_ARG;
+    const Plan p = make_plan(R, N, K, E, flags, num_cus());
+    const GemmArgs a = make_args(xq, xs, packed, offsets, rows, Y, R, T, L, p, nullptr);
+    hipStream_t s = (hipStream_t)stream;
+    return from_hip((flags & FP8_BF16) ? launch_gemm_bf16(a, p, s) : launch_gemm_f16(a, p, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,358 @@
+// rowquant.hip -- the RMS norm (with the residual's addition) and the gated
+// activation, each ending in quantised rows (include/rowquant.h).
+//
+// Both read 16-bit rows once and write the quantised rows in the same pass, so
+// the 16-bit tensor between them and the product never exists in memory.  They
+// are bound by HBM: a lane holds 16 consecutive elements (two 16-byte loads
+// per input, one 16-byte store of codes), so a block of 128 columns is 8
+// neighbouring lanes and an MX block of 32 is 2, and every block maximum is a
+// few lane shuffles.
+//
+// Compiled once per input dtype (ROWQUANT_TU_BF16 = 0 fp16, 1 bf16).
+#include <hip/hip_runtime.h>
+
+#include "rowquant_internal.h"
+
+#ifndef ROWQUANT_TU_BF16
+#define ROWQUANT_TU_BF16 0
+#endif
+
+namespace rowquant {
+
+namespace {
+
+constexpr bool BF16 = ROWQUANT_TU_BF16 != 0;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPiece = 16;   // elements per lane
+// 2^-110: the smallest block maximum an fp8 scale is made from; 448 / it is
+// still a normal number, and so is it / 448.
+constexpr float kTinyMax = 0x1p-110f;
+
+__device__ __forceinline__ float half_to_float(uint32_t h) {
+    if constexpr (BF16) return __uint_as_float(h << 16);
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+
+__device__ __forceinline__ uint32_t float_to_half(float v) {
+    if constexpr (BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+    return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+struct Raw {
+    u32x4 a, b;
+};
+
+__device__ __forceinline__ Raw load16(const uint16_t* p) {
+    Raw r;
+    r.a = __builtin_nontemporal_load((const u32x4*)p);
+    r.b = __builtin_nontemporal_load((const u32x4*)p + 1);
+    return r;
+}
+
+__device__ __forceinline__ Raw zeros16() { return Raw{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}}; }
+
+__device__ __forceinline__ float element(const Raw& r, int i) {
+    const uint32_t w = i < 8 ? r.a[i >> 1] : r.b[(i - 8) >> 1];
+    return half_to_float((i & 1) ? (w >> 16) : (w & 0xFFFFu));
+}
+
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[kPiece]) {
+    u32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = float_to_half(v[2 * i]) | (float_to_half(v[2 * i + 1]) << 16);
+        b[i] = float_to_half(v[8 + 2 * i]) | (float_to_half(v[9 + 2 * i]) << 16);
+    }
+    *(u32x4*)p = a;
+    *((u32x4*)p + 1) = b;
+}
+
+// g / (1 + exp(-g)) through e = exp(-|g|) <= 1, which neither overflows nor
+// loses the quotient: 1 / (1 + e) lies in [1/2, 1].  exp2's argument is split
+// into a rounded product and its remainder (the low part of log2 e included),
+// so e is good to about two units in the last place over the whole range;
+// below exp(-87) e is 0, where the result is under 2^-119 |g|.
+__device__ __forceinline__ float silu(float g) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float m = fmaxf(-fabsf(g), -128.0f);   // e is 0 from there on; keeps l finite
+    const float h = m * kLog2e;
+    const float l = __builtin_fmaf(m, kLog2eLow, __builtin_fmaf(m, kLog2e, -h));
+    float e = __builtin_amdgcn_exp2f(h);
+    e = __builtin_fmaf(e, l * kLn2, e);
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    return g * (g >= 0.0f ? r : e * r);
+}
+
+__device__ __forceinline__ float clamp448(float v) {
+    return __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f);
+}
+
+// 16 values times r as E4M3 codes; v_cvt_pk_fp8_f32 rounds to nearest even.
+__device__ __forceinline__ u32x4 codes16(const float (&v)[kPiece], float r) {
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int w = 0;
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * i] * r), clamp448(v[4 * i + 1] * r), w,
+                                            false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * i + 2] * r), clamp448(v[4 * i + 3] * r),
+                                            w, true);
+        q[i] = (uint32_t)w;
+    }
+    return q;
+}
+
+__device__ __forceinline__ float amax16(const float (&v)[kPiece]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) a = fmaxf(a, fabsf(v[i]));
+    return a;
+}
+
+// The row's int8 scale and its reciprocal (of 1 for a row of zeros).
+struct RowScale {
+    float s, inv;
+};
+
+__device__ __forceinline__ RowScale int8_scale(float amax) {
+    const float s = __fdiv_rn(amax, 127.0f);
+    return {s, __fdiv_rn(1.0f, s > 0.0f ? s : 1.0f)};
+}
+
+// v / s rounded once: the product with the correctly rounded reciprocal,
+// corrected by its exact remainder, then half to even to an integer.  A scale
+// so small that its reciprocal overflows takes the division itself.
+__device__ __forceinline__ uint32_t int8_code(float v, RowScale rs) {
+    float t = v * rs.inv;
+    t = __builtin_fmaf(__builtin_fmaf(-t, rs.s, v), rs.inv, t);
+    const float q = __builtin_amdgcn_fmed3f(rintf(t), -127.0f, 127.0f);
+    return (uint32_t)(int)q & 0xFFu;
+}
+
+// Quantise and store one piece.  Every lane of the wave takes part (the block
+// maxima are shuffles); only live ones store.  at: index of the piece's first
+// element in q; block: index of its 128-block's scale; W: the row length.
+template <int KIND>
+__device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_t at,
+                                     int64_t block, int piece, void* q, void* s, RowScale rs) {
+    if constexpr (KIND == KIND_X16) {
+        if (live) store16((uint16_t*)q + at, v);
+    } else if constexpr (KIND == KIND_INT8) {
+        u32x4 w;
+        if (rs.s > 0.0f && rs.s < 0x1p-125f) {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) {
+                const float t = __builtin_amdgcn_fmed3f(rintf(__fdiv_rn(v[i], rs.s)), -127.f, 127.f);
+                const uint32_t c = ((uint32_t)(int)t & 0xFFu) << (8 * (i & 3));
+                w[i >> 2] = (i & 3) ? (w[i >> 2] | c) : c;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) {
+                const uint32_t c = int8_code(v[i], rs) << (8 * (i & 3));
+                w[i >> 2] = (i & 3) ? (w[i >> 2] | c) : c;
+            }
+        }
+        if (live) *(u32x4*)((uint8_t*)q + at) = w;
+    } else if constexpr (KIND == KIND_FP8) {
+        float a = amax16(v);
+        a = fmaxf(a, __shfl_xor(a, 1, 64));
+        a = fmaxf(a, __shfl_xor(a, 2, 64));
+        a = fmaxf(a, __shfl_xor(a, 4, 64));
+        a = fmaxf(a, kTinyMax);
+        const u32x4 w = codes16(v, __fdiv_rn(448.0f, a));
+        if (live) {
+            *(u32x4*)((uint8_t*)q + at) = w;
+            if ((piece & 7) == 0) ((float*)s)[block] = __fdiv_rn(a, 448.0f);
+        }
+    } else {
+        float a = amax16(v);
+        a = fmaxf(a, __shfl_xor(a, 1, 64));
+        const int ef = (int)(__float_as_uint(a) >> 23);                 // a >= 0
+        const int E = max(ef - 127 - 8, -127);   // floor(log2 a) - 8; subnormal a: -127 as well
+        const u32x4 w = codes16(v, __uint_as_float((uint32_t)(127 - E) << 23));
+        if (live) {
+            *(u32x4*)((uint8_t*)q + at) = w;
+            if ((piece & 1) == 0) ((uint8_t*)s)[at / 32] = (uint8_t)(E + 127);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Kernels that keep a row in registers: one workgroup per row, PPT pieces per
+// thread.  The norm needs the row's sum of squares, the int8 kind its maximum.
+// ---------------------------------------------------------------------------
+
+// op over the workgroup, in every thread; the waves' parts meet in LDS.
+template <int THREADS, bool MAX>
+__device__ __forceinline__ float reduce_row(float x, float* part) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        const float y = __shfl_xor(x, off, 64);
+        x = MAX ? fmaxf(x, y) : x + y;
+    }
+    if constexpr (THREADS > 64) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = part[0];
+#pragma unroll
+        for (int w = 1; w < THREADS / 64; ++w) x = MAX ? fmaxf(x, part[w]) : x + part[w];
+    }
+    return x;
+}
+
+template <int THREADS, int PPT, int KIND, bool NORM>
+__global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
+    __shared__ float part[2][THREADS / 64];
+    const int64_t row = blockIdx.x;
+    const int pieces = (int)(a.W / kPiece);
+    const uint16_t* xa = (const uint16_t*)a.a + row * a.lda;
+    const uint16_t* xb = a.b ? (const uint16_t*)a.b + row * a.ldb : nullptr;
+    float v[PPT][kPiece];
+    float sum = 0.0f;
+    Raw ra[PPT], rb[PPT], rw[PPT];
+#pragma unroll
+    for (int j = 0; j < PPT; ++j) {
+        const int p = threadIdx.x + j * THREADS;
+        ra[j] = p < pieces ? load16(xa + p * kPiece) : zeros16();
+        rb[j] = p < pieces && xb ? load16(xb + p * kPiece) : zeros16();
+        if constexpr (NORM) {
+            rw[j] = zeros16();
+            if (p < pieces) {
+                rw[j].a = *(const u32x4*)((const uint16_t*)a.w + p * kPiece);
+                rw[j].b = *((const u32x4*)((const uint16_t*)a.w + p * kPiece) + 1);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PPT; ++j) {
+        const int p = threadIdx.x + j * THREADS;
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) {
+            if constexpr (NORM) {
+                v[j][i] = element(ra[j], i) + element(rb[j], i);
+                sum = __builtin_fmaf(v[j][i], v[j][i], sum);
+            } else {
+                v[j][i] = silu(element(ra[j], i)) * element(rb[j], i);
+            }
+        }
+        if constexpr (NORM)
+            if (a.h && p < pieces) store16((uint16_t*)a.h + row * a.W + p * kPiece, v[j]);
+    }
+    if constexpr (NORM) {
+        sum = reduce_row<THREADS, false>(sum, part[0]);
+        // IEEE square root and divisions: once per row
+        const float mean = __fdiv_rn(sum, (float)a.W);
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(mean + a.eps));
+#pragma unroll
+        for (int j = 0; j < PPT; ++j)
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) v[j][i] = v[j][i] * r * element(rw[j], i);
+    }
+    RowScale rs{0.0f, 0.0f};
+    if constexpr (KIND == KIND_INT8) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PPT; ++j) m = fmaxf(m, amax16(v[j]));
+        rs = int8_scale(reduce_row<THREADS, true>(m, part[1]));
+        if (threadIdx.x == 0) ((float*)a.s)[row] = rs.s;
+    }
+#pragma unroll
+    for (int j = 0; j < PPT; ++j) {
+        const int p = threadIdx.x + j * THREADS;
+        emit<KIND>(v[j], p < pieces, row * a.W + (int64_t)p * kPiece, row * a.KB + (p >> 3), p, a.q,
+                   a.s, rs);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The gated activation for the kinds that need no maximum of a whole row: 8
+// lanes per (row, block of 128), any number of rows in a workgroup.
+// ---------------------------------------------------------------------------
+constexpr int kFlatThreads = 256;
+
+template <int KIND>
+__global__ __launch_bounds__(kFlatThreads) void swiglu_flat_kernel(RowArgs a) {
+    const int64_t idx = (int64_t)blockIdx.x * kFlatThreads + threadIdx.x;
+    const int64_t item = idx >> 3;
+    const int64_t items = a.T * a.KB;
+    const int64_t row = items >> 32 ? item / a.KB : (int64_t)((uint32_t)item / (uint32_t)a.KB);
+    const int64_t block = item - row * a.KB;
+    const int64_t piece = block * 8 + (idx & 7);
+    const bool live = item < items && piece < a.W / kPiece;
+    Raw rg = zeros16(), ru = zeros16();
+    if (live) {
+        rg = load16((const uint16_t*)a.a + row * a.lda + piece * kPiece);
+        ru = load16((const uint16_t*)a.b + row * a.ldb + piece * kPiece);
+    }
+    float v[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) v[i] = silu(element(rg, i)) * element(ru, i);
+    emit<KIND>(v, live, row * a.W + piece * kPiece, item, (int)(idx & 7), a.q, a.s,
+               RowScale{0.0f, 0.0f});
+}
+
+template <int KIND, bool NORM>
+hipError_t launch_row(const RowArgs& a, hipStream_t stream) {
+    const int64_t pieces = a.W / kPiece;
+    const unsigned grid = (unsigned)a.T;
+    // the fewest threads that hold a row with one piece each, then more pieces
+    if (pieces <= 64)
+        row_kernel<64, 1, KIND, NORM><<<grid, 64, 0, stream>>>(a);
+    else if (pieces <= 256)
+        row_kernel<256, 1, KIND, NORM><<<grid, 256, 0, stream>>>(a);
+    else if (pieces <= 512)
+        row_kernel<512, 1, KIND, NORM><<<grid, 512, 0, stream>>>(a);
+    else if (pieces <= 1024)
+        row_kernel<1024, 1, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
+    else if (pieces <= 2048)
+        row_kernel<1024, 2, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
+    else if (pieces <= 4096)
+        row_kernel<1024, 4, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
+    else if (pieces <= 8192)
+        row_kernel<1024, 8, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
+    else
+        return hipErrorInvalidValue;   // the entry points refuse longer rows
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_flat(const RowArgs& a, hipStream_t stream) {
+    const int64_t threads = a.T * a.KB * 8;
+    const int64_t blocks = (threads + kFlatThreads - 1) / kFlatThreads;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    swiglu_flat_kernel<KIND><<<(unsigned)blocks, kFlatThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm(const RowArgs& a, int kind, hipStream_t stream) {
+    switch (kind) {
+        case KIND_FP8: return launch_row<KIND_FP8, true>(a, stream);
+        case KIND_INT8: return launch_row<KIND_INT8, true>(a, stream);
+        case KIND_MX: return launch_row<KIND_MX, true>(a, stream);
+        default: return launch_row<KIND_X16, true>(a, stream);
+    }
+}
+
+hipError_t launch_swiglu(const RowArgs& a, int kind, hipStream_t stream) {
+    switch (kind) {
+        case KIND_FP8: return launch_flat<KIND_FP8>(a, stream);
+        case KIND_INT8: return launch_row<KIND_INT8, false>(a, stream);
+        case KIND_MX: return launch_flat<KIND_MX>(a, stream);
+        default: return launch_flat<KIND_X16>(a, stream);
+    }
+}
+
+}  // namespace
+
+#if ROWQUANT_TU_BF16
+hipError_t launch_norm_bf16(const RowArgs& a, int kind, hipStream_t s) { return launch_norm(a, kind, s); }
+hipError_t launch_swiglu_bf16(const RowArgs& a, int kind, hipStream_t s) { return launch_swiglu(a, kind, s); }
+#else
+hipError_t launch_norm_f16(const RowArgs& a, int kind, hipStream_t s) { return launch_norm(a, kind, s); }
+hipError_t launch_swiglu_f16(const RowArgs& a, int kind, hipStream_t s) { return launch_swiglu(a, kind, s); }
+#endif
+
+}  // namespace rowquant
