@@ -21,7 +21,7 @@
  * aligned device pointers, stream as void*, asynchronous, nothing allocated,
  * every argument validated on the host before any HIP call).  Shapes: N >= 1,
  * K >= 16 and K % 16 == 0 (else W4A16_ERR_UNSUPPORTED), N, K < 2^24, rows <
- * 2^31, experts <= 65535.  Zero rows are a call without work.
+ * 2^31, the codes of X below 2^36 bytes, experts <= 65535.  Zero rows are a call without work.
  */
 #ifndef FP8_H
 #define FP8_H

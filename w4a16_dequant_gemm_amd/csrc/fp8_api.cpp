@@ -39,6 +39,9 @@ int num_cus() {
     return n;
 }
 
+// The kernels count X in pieces of 16 bytes with 32 bits.
+bool x_fits(int64_t rows, int64_t K) { return (double)rows * (double)K < (double)((int64_t)1 << 36); }
+
 w4a16_status_t check_weights(int64_t E, int64_t K, int64_t N) {
     if (E < 1 || E > kMaxExperts || K < 1 || N < 1 || K >= kMaxDim || N >= kMaxDim)
         return W4A16_ERR_INVALID_ARG;
@@ -51,16 +54,44 @@ w4a16_status_t check_weights(int64_t E, int64_t K, int64_t N) {
 }  // namespace
 
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int cus) {
+    // columns and rows of the tiled kernel's workgroup, by cfg - 1
+    static const int kBn[4] = {256, 128, 64, 64}, kBm[4] = {256, 128, 64, 128};
     Plan p{};
-    (void)N; (void)K; (void)cus;
     const uint32_t hint = flags & FP8_PLAN_MASK;
     const int param = (int)((flags >> W4A16_PLAN_PARAM_SHIFT) & 0xFFu);
+    const int64_t NB = (N + kBlock - 1) / kBlock;
+    const int64_t KB = (K + kBlock - 1) / kBlock;
     const int64_t per = E ? (M + E - 1) / E : M;   // rows an expert has, on average
-    p.variant = STREAM;
-    p.cfg = hint == FP8_PLAN_STREAM && (param == 1 || param == 2) ? param : per <= 16 ? 1 : 2;
-    p.bn = 16;
-    p.bm = 16 * p.cfg;
     p.splits = 1;
+    if (hint == FP8_PLAN_STREAM || (hint != FP8_PLAN_TILED && per <= 32)) {
+        p.variant = STREAM;
+        p.cfg = hint == FP8_PLAN_STREAM && (param == 1 || param == 2) ? param : per <= 16 ? 1 : 2;
+        p.bn = 16;
+        p.bm = 16 * p.cfg;
+        p.tiles = 0;
+        return p;
+    }
+    p.variant = TILED;
+    if (hint == FP8_PLAN_TILED && param >= 1 && param <= 4)
+        p.cfg = param;
+    else
+        p.cfg = per <= 64 ? 3 : per <= 128 ? 4 : per <= 512 ? 2 : 1;
+    p.bn = kBn[p.cfg - 1];
+    p.bm = kBm[p.cfg - 1];
+    const int64_t nbn = (NB * kBlock + p.bn - 1) / p.bn;
+    // grouped: each expert with rows may leave one tile unfilled
+    const int64_t nbm = E ? M / p.bm + (M < E ? M : E) : (M + p.bm - 1) / p.bm;
+    p.tiles = nbm * nbn;
+    if (!E && p.cfg > 1) {
+        // parts of K while a CU would be left without a workgroup, each of 4 blocks at least
+        while (p.splits < 8 && p.tiles * p.splits * 2 <= 2 * (int64_t)cus &&
+               KB >= 8 * p.splits && p.tiles <= (int64_t)(kCounterBytes / 4))
+            p.splits *= 2;
+        const int64_t part = (KB + p.splits - 1) / p.splits;
+        p.splits = (int)((KB + part - 1) / part);      // no empty part
+        if (p.splits > 1)
+            p.workspace = kCounterBytes + (size_t)p.tiles * p.splits * p.bn * p.bm * 4;
+    }
     return p;
 }
 
@@ -86,10 +117,8 @@ GemmArgs make_args(const uint8_t* xq, const float* xs, const void* packed, const
     a.NB = (int)L.NB;
     a.E = (int)L.E;
     a.splits = p.splits;
-    if (p.bn > 0) {
-        a.nbn = (int)((L.N + p.bn - 1) / p.bn);
-        a.nbm = (int)(p.tiles / a.nbn);
-    }
+    a.nbn = (int)((L.NB * kBlock + p.bn - 1) / p.bn);
+    a.nbm = (int)(p.tiles / a.nbn);
     a.s_off = L.s_off;
     a.z_off = L.z_off;
     return a;
@@ -135,6 +164,7 @@ w4a16_status_t fp8_gemm(const uint8_t* xq, const float* xs, const void* packed,
     if (st != W4A16_OK) return st;
     const Layout L = make_layout(1, K, N);
     if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
+    if (!x_fits(M, K)) return W4A16_ERR_INVALID_ARG;
     if (M == 0) return W4A16_OK;
     if (!xq || !xs || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(Y))
         return W4A16_ERR_INVALID_ARG;
@@ -157,6 +187,7 @@ w4a16_status_t fp8_grouped_gemm(const uint8_t* xq, const float* xs, const void* 
     if (st != W4A16_OK) return st;
     const Layout L = make_layout(E, K, N);
     if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
+    if (!x_fits(T, K)) return W4A16_ERR_INVALID_ARG;
     if (R == 0) return W4A16_OK;
     if (!xq || !xs || !offsets || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(offsets) ||
         !aligned16(rows) || !aligned16(Y))

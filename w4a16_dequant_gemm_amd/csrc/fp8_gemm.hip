@@ -222,7 +222,369 @@ hipError_t launch_stream_t(const GemmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Tiled kernel.  A workgroup of WN x WM waves owns BN = 16 NT WN columns and
+// BM = 16 MT WM rows; each wave 16 NT x 16 MT of them.  One step is one block of
+// K: its codes of both operands and its scales go from memory straight to an
+// LDS stage (global loads to LDS: no registers, no ds_write), STAGES in a ring,
+// STAGES - 1 of them in flight, one barrier per step.
+//
+// A stage: the weights' chunks as the blob holds them (a wave reads 64 x 16
+// consecutive bytes), the rows of X of 128 bytes whose eight 16-byte pieces are
+// permuted by p ^ (row / 2) % 8 (the loads choose which global piece a lane
+// fetches, so that 16 lanes that read one piece of 16 rows meet all 64 banks
+// once), and 256 bytes per wave of scales: the first waves fetch the rows'
+// scales, the others the panels'.
+//
+// Task order: an eighth of the tasks, in sequence, to each XCD (workgroups are
+// dealt to XCDs in turn), and inside it GM row tiles by all column tiles, so
+// that the workgroups at work on one XCD share rows and weights in its L2.
+//
+// Grouped: the row tiles of all experts form one list, found from the offsets by
+// a scan over the experts in each wave; the grid is sized for the most there can
+// be and workgroups past the real number leave at once.
+// ---------------------------------------------------------------------------
+
+typedef __attribute__((address_space(1))) const void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// Every lane's 16 (4) bytes at src to dst + 16 (4) * lane; dst is the wave's.
+__device__ __forceinline__ void load16_to_lds(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)dst, 4, 0, 0);
+}
+
+// Until at most N of the wave's loads are under way, then until every wave of
+// the workgroup is here.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Expert and rows of row tile j of the list; total: the list's length.
+struct RowTile {
+    int e;
+    int lo, hi;   // the tile's rows
+};
+
+template <int BM>
+__device__ __forceinline__ int row_tiles_of(const GemmArgs& a, int e) {
+    if (e >= a.E) return 0;
+    const int n = offset_at(a, e + 1) - offset_at(a, e);
+    return n > 0 ? (n + BM - 1) / BM : 0;
+}
+
+__device__ __forceinline__ int scan64(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+template <int BM>
+__device__ __forceinline__ int count_row_tiles(const GemmArgs& a, int lane) {
+    int n = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) n += row_tiles_of<BM>(a, e0 + lane);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d, 64);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+template <int BM>
+__device__ __forceinline__ RowTile find_row_tile(const GemmArgs& a, int j, int lane) {
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+        const int n = row_tiles_of<BM>(a, e0 + lane);
+        const int upto = before + scan64(n, lane);
+        const unsigned long long past = __ballot(upto > j);
+        if (past) {
+            const int first = __ffsll(past) - 1;
+            const int e = e0 + first;
+            const int tile = j - (__shfl(upto, first, 64) - __shfl(n, first, 64));
+            RowTile t;
+            t.e = __builtin_amdgcn_readfirstlane(e);
+            const int lo = offset_at(a, e) + tile * BM;
+            t.lo = __builtin_amdgcn_readfirstlane(lo);
+            t.hi = __builtin_amdgcn_readfirstlane(min(lo + BM, offset_at(a, e + 1)));
+            return t;
+        }
+        before = __shfl(upto, 63, 64);
+    }
+    return RowTile{0, 0, 0};
+}
+
+// Partial tiles of a split K (the protocol of w4a16_gemm.hip: device-scope
+// stores past the XCD's own L2, a device-scope counter, no one waits).
+__device__ __forceinline__ void st_dev(float* p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float ld_dev(const float* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int WN, int WM, int NT, int MT, int STAGES>
+struct Tile {
+    static constexpr int kWaves = WN * WM;
+    static constexpr int BN = 16 * NT * WN;
+    static constexpr int BM = 16 * MT * WM;
+    static constexpr int kWBytes = BN * kBlock;
+    static constexpr int kXBytes = BM * kBlock;
+    static constexpr int kStage = kWBytes + kXBytes + 256 * kWaves;
+    static constexpr int kWLoads = BN / 8 / kWaves;   // 1-KiB loads of a wave per stage
+    static constexpr int kXLoads = BM / 8 / kWaves;
+    static constexpr int kLoads = kWLoads + kXLoads + 1;
+    static constexpr int kLds = STAGES * kStage;
+};
+
+template <int WN, int WM, int NT, int MT, int STAGES, bool GROUPED>
+__global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
+    using C = Tile<WN, WM, NT, MT, STAGES>;
+    constexpr int BM = C::BM;
+    constexpr int GM = 4;
+    static_assert(NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
+    static_assert(C::BM / 64 < C::kWaves, "a wave is left for the weights' scales");
+    extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN;
+    const int wm = wave / WN;
+    const int KB = a.KB;
+
+    // the task: column tile, row tile, part of K
+    const int nbm = GROUPED ? count_row_tiles<BM>(a, lane) : a.nbm;
+    const int64_t total = (int64_t)nbm * a.nbn * a.splits;
+    const int64_t share = (total + 7) / 8;
+    int64_t task = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= share || task >= total) return;
+    const int part = (int)(task % a.splits);
+    const int64_t tile_id = task / a.splits;
+    const int group = (int)(tile_id / ((int64_t)GM * a.nbn));
+    const int in_group = (int)(tile_id - (int64_t)group * GM * a.nbn);
+    const int rows_in = min(nbm - group * GM, GM);
+    const int mb = group * GM + in_group % rows_in;
+    const int nb = in_group / rows_in;
+
+    RowTile rt{0, 0, 0};
+    if constexpr (GROUPED) {
+        rt = find_row_tile<BM>(a, mb, lane);
+    } else {
+        rt.lo = mb * BM;
+        rt.hi = (int)min((int64_t)rt.lo + BM, a.M);
+    }
+    const int tile0 = nb * (C::BN / 16);          // first operand tile of the workgroup
+    const int tiles = a.NB * kPanelTiles;
+    const int per = (KB + a.splits - 1) / a.splits;
+    const int k0 = part * per;
+    const int k1 = min(k0 + per, KB);
+
+    // Global sources of the wave's loads.  The weights': a uniform address and
+    // 16 * lane.  X's: 32 bits per load, counted in pieces of 16 bytes (the entry
+    // points refuse an X of 2^36 bytes), added to a uniform address.
+    const uint8_t* wsrc[C::kWLoads];
+#pragma unroll
+    for (int i = 0; i < C::kWLoads; ++i) {
+        const int c = wave * C::kWLoads + i;
+        const int t = min(tile0 + (c >> 1), tiles - 1);
+        wsrc[i] = a.blob + ((size_t)rt.e * tiles + t) * KB * kChunkBytes + (c & 1) * 1024;
+    }
+    const uint32_t lane16 = 16u * (uint32_t)lane;
+    const uint8_t* zero = a.blob + a.z_off;
+    uint32_t xsrc[C::kXLoads];
+    const auto piece = [&](int i) __attribute__((always_inline)) {   // of the lane, in load i
+        const int r = 8 * (wave * C::kXLoads + i) + (lane >> 3);
+        return (lane & 7) ^ ((r >> 1) & 7);
+    };
+#pragma unroll
+    for (int i = 0; i < C::kXLoads; ++i) {
+        const int r = 8 * (wave * C::kXLoads + i) + (lane >> 3);
+        bool ok;
+        const int64_t row = x_row<GROUPED>(a, min(rt.lo + r, rt.hi - 1), ok);
+        xsrc[i] = (uint32_t)(row * (a.K / 16)) + (uint32_t)piece(i);
+    }
+    const float* sbase;   // uniform; the lane's scales are a row of KB floats from it
+    uint32_t srow;
+    if (wave < BM / 64) {
+        bool ok;
+        sbase = a.xs;
+        srow = (uint32_t)x_row<GROUPED>(a, min(rt.lo + wave * 64 + lane, rt.hi - 1), ok);
+    } else {
+        sbase = (const float*)(a.blob + a.s_off) + (size_t)rt.e * a.NB * KB;
+        srow = (uint32_t)min(tile0 / kPanelTiles + (lane & 1), a.NB - 1);
+    }
+    const float* ssrc = sbase + (size_t)srow * KB;
+
+    auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
+        uint8_t* st = lds + slot * C::kStage;
+#pragma unroll
+        for (int i = 0; i < C::kWLoads; ++i)
+            load16_to_lds(wsrc[i] + (size_t)kb * kChunkBytes + lane16,
+                          st + (wave * C::kWLoads + i) * 1024);
+        uint8_t* xst = st + C::kWBytes;
+        const uint8_t* xbase = a.xq + (size_t)kb * kBlock;
+        if (kb * kBlock + kBlock <= a.K) {
+#pragma unroll
+            for (int i = 0; i < C::kXLoads; ++i)
+                load16_to_lds(xbase + ((size_t)xsrc[i] << 4),
+                              xst + (wave * C::kXLoads + i) * 1024);
+        } else {   // the last block of a K that is no multiple of 128: zeros past its end
+#pragma unroll
+            for (int i = 0; i < C::kXLoads; ++i)
+                load16_to_lds(kb * kBlock + 16 * piece(i) < a.K ? xbase + ((size_t)xsrc[i] << 4)
+                                                                : zero,
+                              xst + (wave * C::kXLoads + i) * 1024);
+        }
+        load4_to_lds(ssrc + kb, xst + C::kXBytes + wave * 256);
+    };
+
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int woff = wn * NT * kChunkBytes + lane * 16;
+    const int xoff = C::kWBytes + wm * MT * kChunkBytes + (lane & 15) * kBlock +
+                     16 * ((2 * (lane >> 4)) ^ ((lane >> 1) & 7));
+    const int xsoff = C::kWBytes + C::kXBytes + 4 * (wm * MT * 16 + (lane & 15));
+    // the wave's panel among the workgroup's: lanes 0 and 1 of the first weights' wave hold them
+    const int wsoff = C::kWBytes + C::kXBytes + 256 * (BM / 64) + 4 * (wn * NT / kPanelTiles);
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (k0 + s < k1) issue(k0 + s, s);
+    int slot = 0;
+    for (int kb = k0; kb < k1; ++kb) {
+        if (kb + STAGES - 2 < k1)
+            stage_barrier<(STAGES - 2) * C::kLoads>();
+        else
+            stage_barrier<0>();
+        if (kb + STAGES - 1 < k1) issue(kb + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+        const uint8_t* st = lds + slot * C::kStage;
+        i32x8 b[MT];
+        float s[MT];
+        const float sw = *(const float*)(st + wsoff);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            b[t] = cat(*(const i32x4*)(st + xoff + t * kChunkBytes),
+                       *(const i32x4*)(st + (xoff ^ 16) + t * kChunkBytes));
+            s[t] = *(const float*)(st + xsoff + 64 * t) * sw;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const i32x8 w = cat(*(const i32x4*)(st + woff + i * kChunkBytes),
+                                *(const i32x4*)(st + woff + i * kChunkBytes + 1024));
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                acc[i][t] = scaled_add(acc[i][t], block_sums(w, b[t]), s[t]);
+        }
+        slot = slot == STAGES - 1 ? 0 : slot + 1;
+    }
+
+    if constexpr (!GROUPED) {
+        if (a.splits > 1) {
+            const int64_t cell = tile_id * a.splits;
+            constexpr int kThreads = C::kWaves * 64;
+            float* mine = a.part + (cell + part) * (int64_t)(BM * C::BN) + tid;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        st_dev(mine + ((i * MT + t) * 4 + r) * kThreads, acc[i][t][r]);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            int* flag = (int*)lds;
+            if (tid == 0)
+                *flag = __hip_atomic_fetch_add(a.cnt + tile_id, 1u, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT) ==
+                        (uint32_t)(a.splits - 1);
+            __syncthreads();
+            if (!*flag) return;
+            if (tid == 0)
+                __hip_atomic_store(a.cnt + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // the last to arrive adds all parts in order: equal calls, equal bits
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int p = 0; p < a.splits; ++p) {
+                const float* src = a.part + (cell + p) * (int64_t)(BM * C::BN) + tid;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][t][r] += ld_dev(src + ((i * MT + t) * 4 + r) * kThreads);
+            }
+        }
+    }
+
+    // a lane has 4 NT consecutive columns of MT rows
+    const int wtile = tile0 + wn * NT;
+    const int n = wtile / kPanelTiles * kBlock + 32 * (lane >> 4) + 4 * (wtile % kPanelTiles);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int m = rt.lo + (wm * MT + t) * 16 + (lane & 15);
+        if (m < rt.hi) {
+            bool ok;
+            x_row<GROUPED>(a, m, ok);
+            uint16_t* y = (uint16_t*)a.Y + (int64_t)m * a.N + n;
+#pragma unroll
+            for (int i = 0; i < NT; i += 2) {
+                f32x4 lo = acc[i][t], hi = acc[i + 1][t];
+                if (!ok) lo = hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if ((a.N & 7) == 0) {   // rows and groups of 8 columns are 16-byte aligned
+                    if (n + 4 * i < a.N) {
+                        i32x4 v;
+                        v[0] = (int)(to_half(lo[0]) | (to_half(lo[1]) << 16));
+                        v[1] = (int)(to_half(lo[2]) | (to_half(lo[3]) << 16));
+                        v[2] = (int)(to_half(hi[0]) | (to_half(hi[1]) << 16));
+                        v[3] = (int)(to_half(hi[2]) | (to_half(hi[3]) << 16));
+                        *(i32x4*)(y + 4 * i) = v;
+                    }
+                } else {
+                    store4(a.Y, m, n + 4 * i, a.N, lo);
+                    store4(a.Y, m, n + 4 * i + 4, a.N, hi);
+                }
+            }
+        }
+    }
+}
+
+template <int WN, int WM, int NT, int MT, int STAGES>
+hipError_t launch_tiled_t(const GemmArgs& a, const Plan& p, hipStream_t stream) {
+    using C = Tile<WN, WM, NT, MT, STAGES>;
+    if (p.bn != C::BN || p.bm != C::BM) return hipErrorInvalidValue;   // plan and kernel agree
+    const int64_t grid = (p.tiles * p.splits + 7) / 8 * 8;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (a.offsets)
+        fp8_tiled_kernel<WN, WM, NT, MT, STAGES, true>
+            <<<(unsigned)grid, C::kWaves * 64, C::kLds, stream>>>(a);
+    else
+        fp8_tiled_kernel<WN, WM, NT, MT, STAGES, false>
+            <<<(unsigned)grid, C::kWaves * 64, C::kLds, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_tiled(const GemmArgs& a, const Plan& p, hipStream_t stream) {
+    switch (p.cfg) {
+        case 1: return launch_tiled_t<2, 4, 8, 4, 2>(a, p, stream);   // 132 KiB of LDS
+        case 2: return launch_tiled_t<2, 2, 4, 4, 2>(a, p, stream);   // 66 KiB: two per CU
+        case 3: return launch_tiled_t<2, 2, 2, 2, 4>(a, p, stream);   // 68 KiB
+        default: return launch_tiled_t<2, 2, 2, 4, 3>(a, p, stream);  // 75 KiB
+    }
+}
+
 hipError_t launch(const GemmArgs& a, const Plan& p, hipStream_t stream) {
+    if (p.variant == TILED) return launch_tiled(a, p, stream);
     if (p.cfg == 1) return launch_stream_t<1, 1, 4>(a, stream);
     return launch_stream_t<2, 1, 4>(a, stream);
 }
