@@ -138,7 +138,9 @@ def _stream_handle(stream) -> int:
     """hipStream_t of `stream` (a torch stream, a raw handle, or None = torch's
     current stream on the current device) as an integer."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # what torch.cuda.current_stream().cuda_stream holds, without making a stream
+        # object (0.2 against 3.0 us per call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
             const int64_t m = min(m0 + 16 * t + (lane & 15), hi - 1);
             bool ok;
             const int64_t r = x_row<GROUPED>(a, m, ok);
-            xsrc[t] = a.xq + r * a.K + 32 * g;
+            xsrc[t] = a.xq + r * a.K + 16 * g;
             xscale[t] = a.xs + r * KB;
         }
         f32x4 acc[MT][NT];
@@ -152,12 +152,12 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
                 wb[slot][j][1] = __builtin_nontemporal_load(p + 64);
             }
             sw[slot] = wscale[kb];
-            const int left = a.K - kb * kBlock - 32 * g;   // bytes of the row from the lane's on
+            const int left = a.K - kb * kBlock - 16 * g;   // bytes of the row from the lane's on
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const uint8_t* p = xsrc[t] + kb * kBlock;
                 xb[slot][t][0] = *(const i32x4*)(left > 0 ? p : zero);
-                xb[slot][t][1] = *(const i32x4*)(left > 16 ? p + 16 : zero);
+                xb[slot][t][1] = *(const i32x4*)(left > 64 ? p + 64 : zero);
                 sx[slot][t] = xscale[t][kb];
             }
         };
@@ -256,11 +256,18 @@ __device__ __forceinline__ void load4_to_lds(const void* src, void* dst) {
     __builtin_amdgcn_global_load_lds((GlobalPtr)src, (LdsPtr)dst, 4, 0, 0);
 }
 
-// Until at most N of the wave's loads are under way, then until every wave of
-// the workgroup is here.
+// v as a value the compiler cannot compute ahead of the loop: addresses made
+// from it take registers only while they are used.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Until at most N of the wave's loads are under way and its reads of LDS are done,
+// then until every wave of the workgroup is here.
 template <int N>
 __device__ __forceinline__ void stage_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // Expert and rows of row tile j of the list; total: the list's length.
@@ -341,11 +348,15 @@ struct Tile {
 };
 
 template <int WN, int WM, int NT, int MT, int STAGES, bool GROUPED>
-__global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
+__global__ __launch_bounds__(WN* WM * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+fp8_tiled_kernel(GemmArgs a) {
     using C = Tile<WN, WM, NT, MT, STAGES>;
     constexpr int BM = C::BM;
     constexpr int GM = 4;
-    static_assert(NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
+    constexpr bool SPREAD = STAGES == 2;
+    constexpr int kEvery = NT * MT >= 2 * C::kLoads ? 2 : 1;   // tiles from load to load
+    static_assert(!SPREAD || NT * MT / kEvery >= C::kLoads, "every load has a place");
+    static_assert(NT % 2 == 0 && NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
     static_assert(C::BM / 64 < C::kWaves, "a wave is left for the weights' scales");
     extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
 
@@ -396,16 +407,16 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
     const uint32_t lane16 = 16u * (uint32_t)lane;
     const uint8_t* zero = a.blob + a.z_off;
     uint32_t xsrc[C::kXLoads];
-    const auto piece = [&](int i) __attribute__((always_inline)) {   // of the lane, in load i
-        const int r = 8 * (wave * C::kXLoads + i) + (lane >> 3);
-        return (lane & 7) ^ ((r >> 1) & 7);
+    const auto piece = [&](int l, int i) __attribute__((always_inline)) {   // of lane l, in load i
+        const int r = 8 * (wave * C::kXLoads + i) + (l >> 3);
+        return (l & 7) ^ ((r >> 1) & 7);
     };
 #pragma unroll
     for (int i = 0; i < C::kXLoads; ++i) {
         const int r = 8 * (wave * C::kXLoads + i) + (lane >> 3);
         bool ok;
         const int64_t row = x_row<GROUPED>(a, min(rt.lo + r, rt.hi - 1), ok);
-        xsrc[i] = (uint32_t)(row * (a.K / 16)) + (uint32_t)piece(i);
+        xsrc[i] = (uint32_t)(row * (a.K / 16)) + (uint32_t)piece(lane, i);
     }
     const float* sbase;   // uniform; the lane's scales are a row of KB floats from it
     uint32_t srow;
@@ -417,29 +428,28 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
         sbase = (const float*)(a.blob + a.s_off) + (size_t)rt.e * a.NB * KB;
         srow = (uint32_t)min(tile0 / kPanelTiles + (lane & 1), a.NB - 1);
     }
-    const float* ssrc = sbase + (size_t)srow * KB;
+    const uint32_t ssrc = srow * (uint32_t)KB * 4u;   // below 2^36 / 32 bytes
 
-    auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
+    // Load q of the wave's kLoads of a stage.  In the last block of a K that is no
+    // multiple of 128 the lanes past its end read zeros.
+    auto issue_one = [&](int q, int kb, int slot) __attribute__((always_inline)) {
         uint8_t* st = lds + slot * C::kStage;
-#pragma unroll
-        for (int i = 0; i < C::kWLoads; ++i)
-            load16_to_lds(wsrc[i] + (size_t)kb * kChunkBytes + lane16,
-                          st + (wave * C::kWLoads + i) * 1024);
         uint8_t* xst = st + C::kWBytes;
-        const uint8_t* xbase = a.xq + (size_t)kb * kBlock;
-        if (kb * kBlock + kBlock <= a.K) {
-#pragma unroll
-            for (int i = 0; i < C::kXLoads; ++i)
-                load16_to_lds(xbase + ((size_t)xsrc[i] << 4),
-                              xst + (wave * C::kXLoads + i) * 1024);
-        } else {   // the last block of a K that is no multiple of 128: zeros past its end
-#pragma unroll
-            for (int i = 0; i < C::kXLoads; ++i)
-                load16_to_lds(kb * kBlock + 16 * piece(i) < a.K ? xbase + ((size_t)xsrc[i] << 4)
-                                                                : zero,
-                              xst + (wave * C::kXLoads + i) * 1024);
+        if (q < C::kWLoads) {
+            load16_to_lds(wsrc[q] + (size_t)kb * kChunkBytes + lane16,
+                          st + (wave * C::kWLoads + q) * 1024);
+        } else if (q < C::kWLoads + C::kXLoads) {
+            const int i = q - C::kWLoads;
+            const uint8_t* src = a.xq + (size_t)kb * kBlock + ((size_t)fresh(xsrc[i]) << 4);
+            if (kb * kBlock + 16 * piece(lane, i) >= a.K) src = zero;
+            load16_to_lds(src, xst + (wave * C::kXLoads + i) * 1024);
+        } else {
+            load4_to_lds((const uint8_t*)(sbase + kb) + ssrc, xst + C::kXBytes + wave * 256);
         }
-        load4_to_lds(ssrc + kb, xst + C::kXBytes + wave * 256);
+    };
+    auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < C::kLoads; ++q) issue_one(q, kb, slot);
     };
 
     f32x4 acc[NT][MT];
@@ -449,8 +459,8 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
         for (int t = 0; t < MT; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int woff = wn * NT * kChunkBytes + lane * 16;
-    const int xoff = C::kWBytes + wm * MT * kChunkBytes + (lane & 15) * kBlock +
-                     16 * ((2 * (lane >> 4)) ^ ((lane >> 1) & 7));
+    const int xoff = C::kWBytes + (wm * MT * 16 + (lane & 15)) * kBlock +
+                     16 * ((lane >> 4) ^ ((lane >> 1) & 7));
     const int xsoff = C::kWBytes + C::kXBytes + 4 * (wm * MT * 16 + (lane & 15));
     // the wave's panel among the workgroup's: lanes 0 and 1 of the first weights' wave hold them
     const int wsoff = C::kWBytes + C::kXBytes + 256 * (BM / 64) + 4 * (wn * NT / kPanelTiles);
@@ -459,32 +469,70 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void fp8_tiled_kernel(GemmArgs a) {
     for (int s = 0; s < STAGES - 1; ++s)
         if (k0 + s < k1) issue(k0 + s, s);
     int slot = 0;
+    // The multiply-adds of a tile follow kLag tiles behind its matrix instruction,
+    // across steps too, so that neither waits for the other: ring holds the sums
+    // under way, s_old the scales of the step before.
+    constexpr int kTiles = NT * MT;
+    constexpr int kLag = 3;
+    static_assert(kTiles % (kLag + 1) == 0, "the ring's places are fixed");
+    f32x4 ring[kLag + 1];
+    float s_old[MT];
+#pragma unroll
+    for (int q = 0; q <= kLag; ++q) ring[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int t = 0; t < MT; ++t) s_old[t] = 0.0f;
     for (int kb = k0; kb < k1; ++kb) {
+        const int free_slot = slot == 0 ? STAGES - 1 : slot - 1;
         if (kb + STAGES - 2 < k1)
             stage_barrier<(STAGES - 2) * C::kLoads>();
         else
             stage_barrier<0>();
-        if (kb + STAGES - 1 < k1) issue(kb + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+        if constexpr (!SPREAD)
+            if (kb + STAGES - 1 < k1) issue(kb + STAGES - 1, free_slot);
         const uint8_t* st = lds + slot * C::kStage;
-        i32x8 b[MT];
+        i32x8 b[MT], w[3];
         float s[MT];
-        const float sw = *(const float*)(st + wsoff);
+        auto read_w = [&](int i) __attribute__((always_inline)) {
+            const uint8_t* wp = st + woff + i * kChunkBytes;
+            w[i % 3] = cat(*(const i32x4*)wp, *(const i32x4*)(wp + 1024));
+        };
+        read_w(0);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            b[t] = cat(*(const i32x4*)(st + xoff + t * kChunkBytes),
-                       *(const i32x4*)(st + (xoff ^ 16) + t * kChunkBytes));
-            s[t] = *(const float*)(st + xsoff + 64 * t) * sw;
+            const uint8_t* x = st + t * kChunkBytes;
+            b[t] = cat(*(const i32x4*)(x + xoff), *(const i32x4*)(x + (xoff ^ 64)));
+        }
+        read_w(1);
+        const float sw = *(const float*)(st + wsoff);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) s[t] = *(const float*)(st + xsoff + 64 * t) * sw;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            const int i = j / MT, t = j % MT;
+            if (t == 0 && i + 2 < NT) read_w(i + 2);
+            if constexpr (SPREAD) {
+                // one load of the next stage every few tiles: issued all at once they would
+                // hold up the reads behind them (past the last block: that block once more)
+                if (j % kEvery == 0 && j / kEvery < C::kLoads)
+                    issue_one(j / kEvery, min(kb + 1, k1 - 1), free_slot);
+            }
+            f32x4 next = block_sums(w[i % 3], b[t]);
+            const int l = j < kLag ? j - kLag + kTiles : j - kLag;
+            f32x4 done = ring[(j + 1) % (kLag + 1)];
+            asm volatile("" : "+v"(next), "+v"(done));   // keeps this order
+            acc[l / MT][l % MT] =
+                scaled_add(acc[l / MT][l % MT], done, j < kLag ? s_old[l % MT] : s[l % MT]);
+            ring[j % (kLag + 1)] = next;
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const i32x8 w = cat(*(const i32x4*)(st + woff + i * kChunkBytes),
-                                *(const i32x4*)(st + woff + i * kChunkBytes + 1024));
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                acc[i][t] = scaled_add(acc[i][t], block_sums(w, b[t]), s[t]);
-        }
+        for (int t = 0; t < MT; ++t) s_old[t] = s[t];
         slot = slot == STAGES - 1 ? 0 : slot + 1;
     }
+#pragma unroll
+    for (int l = kTiles - kLag; l < kTiles; ++l)
+        acc[l / MT][l % MT] = scaled_add(acc[l / MT][l % MT], ring[l % (kLag + 1)], s_old[l % MT]);
+    // no load to LDS outlives the workgroup
+    if constexpr (SPREAD) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     if constexpr (!GROUPED) {
         if (a.splits > 1) {

@@ -5,8 +5,8 @@
 // Both operands of v_mfma_f32_16x16x128_f8f6f4 give lane l row (of A) or
 // column (of B) l % 16 and 32 bytes of the 128 reduction indices.  The sum
 // over k does not depend on which index a byte stands for as long as A and B
-// agree, so lane l takes the 32 consecutive bytes k = 32 * (l / 16) .. +31 of
-// a block in both.  The weights are A, so an accumulator register of lane l is
+// agree; lane l takes the 16 bytes from k = 16 * (l / 16) and the 16 from 64 +
+// 16 * (l / 16) in both.  The weights are A, so an accumulator register of lane l is
 // X row l % 16 and weight row 4 * (l / 16) + r: one lane has one row of X, and
 // the two scales of a block are one number per lane.
 //

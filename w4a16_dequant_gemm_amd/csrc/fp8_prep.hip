@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kThreads) void repack_codes(const uint8_t* __restri
         const int64_t e = panel / NB;
         const int j = lane & 15;
         const int64_t n = (panel - e * NB) * kBlock + 32 * (j >> 2) + 4 * i + (j & 3);
-        const int64_t k = kb * kBlock + 32 * (lane >> 4) + 16 * half;
+        const int64_t k = kb * kBlock + 16 * (lane >> 4) + 64 * half;
         u32x4 v = {0u, 0u, 0u, 0u};
         if (n < N && k < K) v = *(const u32x4*)(w + (e * N + n) * K + k);
         *(u32x4*)(out + idx * 16) = v;

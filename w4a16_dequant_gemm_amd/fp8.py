@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _ptr, _require, _stream, load_library, workspace_for)
+               _bad, _check, _ptr, _require, _stream, _stream_handle, load_library, workspace_for)
 
 FP8_LAYOUT_VERSION = 1
 FP8_BLOCK = 128
@@ -26,13 +26,14 @@ C_FUNCTIONS_FP8 = ("fp8_packed_bytes", "fp8_repack", "fp8_workspace_bytes", "fp8
 _DT = {"fp16": (0x0, torch.float16), "bf16": (0x1, torch.bfloat16)}
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
-_declared = False
+_declared = None
+_ws_bytes = {}
 
 
 def _lib():
     global _declared
-    lib = load_library()
-    if not _declared:
+    if _declared is None:
+        lib = load_library()
         p, i64, ci, u32, sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32,
                                ctypes.c_size_t)
         lib.fp8_packed_bytes.argtypes = [i64, i64, i64]
@@ -45,8 +46,8 @@ def _lib():
         lib.fp8_gemm.restype = ci
         lib.fp8_grouped_gemm.argtypes = [p, p, p, sz, p, p, p, i64, i64, i64, i64, i64, u32, p]
         lib.fp8_grouped_gemm.restype = ci
-        _declared = True
-    return lib
+        _declared = lib
+    return _declared
 
 
 def plan_flags_fp8(plan) -> int:
@@ -109,10 +110,22 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
         _bad(f"{where}: xq has K = {K}, the blob {packed.K}")
     if out not in _DT:
         raise ValueError(f"bad output dtype {out!r}")
-    _require(xs, f"{where}: xs", torch.float32, rows * _blocks(K), xq.device)
-    if packed.data.device != xq.device:
+    dev = xq.get_device()
+    if (xs.dtype != torch.float32 or xs.numel() != rows * _blocks(K) or not xs.is_contiguous()
+            or xs.get_device() != dev):
+        _require(xs, f"{where}: xs", torch.float32, rows * _blocks(K), xq.device)   # raises
+    if packed.data.get_device() != dev:
         _bad(f"{where}: the blob is on another device")
     return rows, K, *_DT[out]
+
+
+def _workspace_need(M: int, N: int, K: int, flags: int) -> int:
+    # the plan depends on the shape and the flags only
+    key = (M, N, K, flags)
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = _ws_bytes[key] = fp8_workspace_bytes(M, N, K, flags)
+    return need
 
 
 def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "bf16",
@@ -126,14 +139,16 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
     N = packed.N
     if Y is None:
         Y = torch.empty((M, N), dtype=tdt, device=xq.device)
-    _require(Y, "fp8_gemm: Y", tdt, M * N, xq.device)
-    flags = flag | plan_flags_fp8(plan)
+    else:
+        _require(Y, "fp8_gemm: Y", tdt, M * N, xq.device)
+    flags = flag if plan is None else flag | plan_flags_fp8(plan)
     if workspace is None:
-        workspace = workspace_for(fp8_workspace_bytes(M, N, K, flags), xq.device, stream)
-    _check(_lib().fp8_gemm(_ptr(xq), _ptr(xs), _ptr(packed.data), packed.data.numel(), _ptr(Y), M,
-                           N, K, flags, _ptr(workspace),
-                           0 if workspace is None else workspace.numel(), _stream(stream)),
-           "fp8_gemm")
+        workspace = workspace_for(_workspace_need(M, N, K, flags), xq.device, stream)
+    _check(_lib().fp8_gemm(xq.data_ptr(), xs.data_ptr(), packed.data.data_ptr(),
+                           packed.data.numel(), Y.data_ptr(), M, N, K, flags,
+                           None if workspace is None else workspace.data_ptr(),
+                           0 if workspace is None else workspace.numel(),
+                           _stream_handle(stream)), "fp8_gemm")
     return Y
 
 
@@ -143,17 +158,21 @@ def fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, offs
     """Y [R][N]: rows offsets[e] .. offsets[e+1]-1 are rows of xq times the weights of expert e.
     offsets int32 [E+1] on the device (never read by the host); output row r is made from row
     rows[r] of xq (int32 [R]), or from row r if rows is None (then R = xq.shape[0])."""
-    T, K, flag, tdt = _rows("fp8_grouped_gemm", xq, xs, packed, out)
+    where = "fp8_grouped_gemm"
+    T, K, flag, tdt = _rows(where, xq, xs, packed, out)
     E, N = packed.E, packed.N
-    _require(offsets, "fp8_grouped_gemm: offsets", torch.int32, E + 1, xq.device)
-    R = T if rows is None else rows.numel()
+    _require(offsets, f"{where}: offsets", torch.int32, E + 1, xq.device)
+    R = T
     if rows is not None:
-        _require(rows, "fp8_grouped_gemm: rows", torch.int32, R, xq.device)
+        R = rows.numel()
+        _require(rows, f"{where}: rows", torch.int32, R, xq.device)
     if Y is None:
         Y = torch.empty((R, N), dtype=tdt, device=xq.device)
-    _require(Y, "fp8_grouped_gemm: Y", tdt, R * N, xq.device)
-    _check(_lib().fp8_grouped_gemm(_ptr(xq), _ptr(xs), _ptr(packed.data), packed.data.numel(),
-                                   _ptr(offsets), _ptr(rows), _ptr(Y), R, T, E, N, K,
-                                   flag | plan_flags_fp8(plan), _stream(stream)),
-           "fp8_grouped_gemm")
+    else:
+        _require(Y, f"{where}: Y", tdt, R * N, xq.device)
+    flags = flag if plan is None else flag | plan_flags_fp8(plan)
+    _check(_lib().fp8_grouped_gemm(xq.data_ptr(), xs.data_ptr(), packed.data.data_ptr(),
+                                   packed.data.numel(), offsets.data_ptr(),
+                                   None if rows is None else rows.data_ptr(), Y.data_ptr(), R, T,
+                                   E, N, K, flags, _stream_handle(stream)), where)
     return Y
