@@ -347,15 +347,31 @@ struct Tile {
     static constexpr int kLds = STAGES * kStage;
 };
 
+// The order of a wave's tiles within a step where the next step's operands are read
+// ahead: column tiles 0, 1 and NT-2, NT-1 row tile by row tile, those between column by
+// column.  read_at(i): the place before which column tile i is read, its register set
+// (one of four) being free then.
+template <int NT, int MT>
+struct TileOrder {
+    static constexpr int J = (NT - 2) * MT;
+    static constexpr int col(int j) {
+        return j < 2 * MT ? j % 2 : j >= J ? NT - 2 + (j - J) % 2 : j / MT;
+    }
+    static constexpr int row(int j) {
+        return j < 2 * MT ? j / 2 : j >= J ? (j - J) / 2 : j % MT;
+    }
+    static constexpr int read_at(int i) {
+        return i < 4 ? i - 2 : i < 6 ? 2 * MT : (i - 3) * MT;
+    }
+};
+
 template <int WN, int WM, int NT, int MT, int STAGES, bool GROUPED>
 __global__ __launch_bounds__(WN* WM * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 fp8_tiled_kernel(GemmArgs a) {
     using C = Tile<WN, WM, NT, MT, STAGES>;
     constexpr int BM = C::BM;
     constexpr int GM = 4;
-    constexpr bool SPREAD = STAGES == 2;
-    constexpr int kEvery = NT * MT >= 2 * C::kLoads ? 2 : 1;   // tiles from load to load
-    static_assert(!SPREAD || NT * MT / kEvery >= C::kLoads, "every load has a place");
+    constexpr bool AHEAD = STAGES == 2;
     static_assert(NT % 2 == 0 && NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
     static_assert(C::BM / 64 < C::kWaves, "a wave is left for the weights' scales");
     extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
@@ -465,10 +481,6 @@ fp8_tiled_kernel(GemmArgs a) {
     // the wave's panel among the workgroup's: lanes 0 and 1 of the first weights' wave hold them
     const int wsoff = C::kWBytes + C::kXBytes + 256 * (BM / 64) + 4 * (wn * NT / kPanelTiles);
 
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (k0 + s < k1) issue(k0 + s, s);
-    int slot = 0;
     // The multiply-adds of a tile follow kLag tiles behind its matrix instruction,
     // across steps too, so that neither waits for the other: ring holds the sums
     // under way, s_old the scales of the step before.
@@ -476,63 +488,129 @@ fp8_tiled_kernel(GemmArgs a) {
     constexpr int kLag = 3;
     static_assert(kTiles % (kLag + 1) == 0, "the ring's places are fixed");
     f32x4 ring[kLag + 1];
-    float s_old[MT];
+    float s[MT], s_old[MT];
 #pragma unroll
     for (int q = 0; q <= kLag; ++q) ring[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < MT; ++t) s_old[t] = 0.0f;
-    for (int kb = k0; kb < k1; ++kb) {
-        const int free_slot = slot == 0 ? STAGES - 1 : slot - 1;
-        if (kb + STAGES - 2 < k1)
-            stage_barrier<(STAGES - 2) * C::kLoads>();
-        else
-            stage_barrier<0>();
-        if constexpr (!SPREAD)
-            if (kb + STAGES - 1 < k1) issue(kb + STAGES - 1, free_slot);
-        const uint8_t* st = lds + slot * C::kStage;
-        i32x8 b[MT], w[3];
-        float s[MT];
-        auto read_w = [&](int i) __attribute__((always_inline)) {
-            const uint8_t* wp = st + woff + i * kChunkBytes;
-            w[i % 3] = cat(*(const i32x4*)wp, *(const i32x4*)(wp + 1024));
-        };
-        read_w(0);
+    i32x8 b[MT];
+    auto read_x = [&](const uint8_t* st, int t) __attribute__((always_inline)) {
+        const uint8_t* x = st + t * kChunkBytes;
+        b[t] = cat(*(const i32x4*)(x + xoff), *(const i32x4*)(x + (xoff ^ 64)));
+    };
+    auto read_w = [&](const uint8_t* st, int i) __attribute__((always_inline)) {
+        const uint8_t* wp = st + woff + i * kChunkBytes;
+        return cat(*(const i32x4*)wp, *(const i32x4*)(wp + 1024));
+    };
+    auto multiply = [&](int i, int t, int li, int lt, float ls, int j, const i32x8& w)
+                        __attribute__((always_inline)) {
+        f32x4 next = block_sums(w, b[t]);
+        f32x4 done = ring[(j + 1) % (kLag + 1)];
+        asm volatile("" : "+v"(next), "+v"(done));   // keeps this order
+        acc[li][lt] = scaled_add(acc[li][lt], done, ls);
+        ring[j % (kLag + 1)] = next;
+    };
+
+    if constexpr (AHEAD) {
+        // The barrier that hands over a stage stands before the last two column tiles of
+        // the step before: their operands are in registers, all reads of the old stage
+        // are done, so its slot is free for the block after the next, and the next step's
+        // first operands are read while these tiles multiply.  The first and the last two
+        // column tiles go row tile by row tile, so that b[t] is free (and needed) early.
+        using O = TileOrder<NT, MT>;
+        constexpr int J = (NT - 2) * MT;
+        static_assert(2 * MT >= C::kLoads - 1, "every load has a place");
+        i32x8 w[4];
+        issue(k0, 0);
+        stage_barrier<0>();
+        issue(min(k0 + 1, k1 - 1), 1);
+        w[0] = read_w(lds, 0);
+        w[1] = read_w(lds, 1);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const uint8_t* x = st + t * kChunkBytes;
-            b[t] = cat(*(const i32x4*)(x + xoff), *(const i32x4*)(x + (xoff ^ 64)));
+            read_x(lds, t);
+            s[t] = *(const float*)(lds + xsoff + 64 * t) * *(const float*)(lds + wsoff);
         }
-        read_w(1);
-        const float sw = *(const float*)(st + wsoff);
+        for (int kb = k0; kb < k1; ++kb) {
+            const uint8_t* st = lds + ((kb - k0) & 1) * C::kStage;
+            const uint8_t* next = lds + ((kb - k0 + 1) & 1) * C::kStage;
+            float s_new[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) s[t] = *(const float*)(st + xsoff + 64 * t) * sw;
+            for (int j = 0; j < kTiles; ++j) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-            const int i = j / MT, t = j % MT;
-            if (t == 0 && i + 2 < NT) read_w(i + 2);
-            if constexpr (SPREAD) {
-                // one load of the next stage every few tiles: issued all at once they would
-                // hold up the reads behind them (past the last block: that block once more)
-                if (j % kEvery == 0 && j / kEvery < C::kLoads)
-                    issue_one(j / kEvery, min(kb + 1, k1 - 1), free_slot);
+                for (int i = 2; i < NT; ++i)
+                    if (O::read_at(i) == j) w[i % 4] = read_w(st, i);
+                if (j == J) {
+                    asm volatile("" : "+v"(w[(NT - 2) % 4]), "+v"(w[(NT - 1) % 4]));   // are here
+                    stage_barrier<0>();
+                    w[0] = read_w(next, 0);
+                }
+                if (j == J + 1) w[1] = read_w(next, 1);
+                if (j >= J) {
+                    // past the last block: that block once more, which no one reads
+                    issue_one(j - J, min(kb + 2, k1 - 1), (kb - k0) & 1);
+                    if (j == kTiles - 1)
+#pragma unroll
+                        for (int q = kTiles - J; q < C::kLoads; ++q)
+                            issue_one(q, min(kb + 2, k1 - 1), (kb - k0) & 1);
+                    if (j > J && (j - J) % 2 == 0) read_x(next, (j - J) / 2 - 1);
+                    if (j == J)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+                            s_new[t] = *(const float*)(next + xsoff + 64 * t) *
+                                       *(const float*)(next + wsoff);
+                }
+                const int l = j < kLag ? j - kLag + kTiles : j - kLag;
+                multiply(O::col(j), O::row(j), O::col(l), O::row(l),
+                         j < kLag ? s_old[O::row(l)] : s[O::row(l)], j, w[O::col(j) % 4]);
             }
-            f32x4 next = block_sums(w[i % 3], b[t]);
-            const int l = j < kLag ? j - kLag + kTiles : j - kLag;
-            f32x4 done = ring[(j + 1) % (kLag + 1)];
-            asm volatile("" : "+v"(next), "+v"(done));   // keeps this order
-            acc[l / MT][l % MT] =
-                scaled_add(acc[l / MT][l % MT], done, j < kLag ? s_old[l % MT] : s[l % MT]);
-            ring[j % (kLag + 1)] = next;
+            read_x(next, MT - 1);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                s_old[t] = s[t];
+                s[t] = s_new[t];
+            }
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) s_old[t] = s[t];
-        slot = slot == STAGES - 1 ? 0 : slot + 1;
-    }
+        for (int l = kTiles - kLag; l < kTiles; ++l)
+            acc[O::col(l)][O::row(l)] =
+                scaled_add(acc[O::col(l)][O::row(l)], ring[l % (kLag + 1)], s_old[O::row(l)]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load to LDS outlives the workgroup
+    } else {
 #pragma unroll
-    for (int l = kTiles - kLag; l < kTiles; ++l)
-        acc[l / MT][l % MT] = scaled_add(acc[l / MT][l % MT], ring[l % (kLag + 1)], s_old[l % MT]);
-    // no load to LDS outlives the workgroup
-    if constexpr (SPREAD) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        for (int q = 0; q < STAGES - 1; ++q)
+            if (k0 + q < k1) issue(k0 + q, q);
+        int slot = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+            if (kb + STAGES - 2 < k1)
+                stage_barrier<(STAGES - 2) * C::kLoads>();
+            else
+                stage_barrier<0>();
+            if (kb + STAGES - 1 < k1) issue(kb + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+            const uint8_t* st = lds + slot * C::kStage;
+            i32x8 w[NT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) read_x(st, t);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) w[i] = read_w(st, i);
+            const float sw = *(const float*)(st + wsoff);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s[t] = *(const float*)(st + xsoff + 64 * t) * sw;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                const int l = j < kLag ? j - kLag + kTiles : j - kLag;
+                multiply(j / MT, j % MT, l / MT, l % MT, j < kLag ? s_old[l % MT] : s[l % MT], j,
+                         w[j / MT]);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s_old[t] = s[t];
+            slot = slot == STAGES - 1 ? 0 : slot + 1;
+        }
+#pragma unroll
+        for (int l = kTiles - kLag; l < kTiles; ++l)
+            acc[l / MT][l % MT] =
+                scaled_add(acc[l / MT][l % MT], ring[l % (kLag + 1)], s_old[l % MT]);
+    }
 
     if constexpr (!GROUPED) {
         if (a.splits > 1) {
