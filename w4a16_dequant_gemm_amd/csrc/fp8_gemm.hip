@@ -519,11 +519,14 @@ fp8_tiled_kernel(GemmArgs a) {
         // column tiles go row tile by row tile, so that b[t] is free (and needed) early.
         using O = TileOrder<NT, MT>;
         constexpr int J = (NT - 2) * MT;
-        static_assert(2 * MT >= C::kLoads - 1, "every load has a place");
+        constexpr int kEvery = kTiles >= 3 * C::kLoads ? 2 : 1;
+        static_assert(kEvery * C::kLoads <= kTiles, "every load has its place before the barrier");
         i32x8 w[4];
         issue(k0, 0);
         stage_barrier<0>();
-        issue(min(k0 + 1, k1 - 1), 1);
+#pragma unroll
+        for (int q = 0; kEvery * q < kTiles - J; ++q)   // the others follow in the first step
+            if (q < C::kLoads) issue_one(q, min(k0 + 1, k1 - 1), 1);
         w[0] = read_w(lds, 0);
         w[1] = read_w(lds, 1);
 #pragma unroll
@@ -546,13 +549,13 @@ fp8_tiled_kernel(GemmArgs a) {
                     w[0] = read_w(next, 0);
                 }
                 if (j == J + 1) w[1] = read_w(next, 1);
+                // one load in kEvery tiles: more at once would hold up the reads and tiles
+                // behind them.  Past the last block: that block once more, which no one reads.
+                if ((j + kTiles - J) % kTiles % kEvery == 0 &&
+                    (j + kTiles - J) % kTiles / kEvery < C::kLoads)
+                    issue_one((j + kTiles - J) % kTiles / kEvery,
+                              min(kb + (j >= J ? 2 : 1), k1 - 1), (kb - k0 + (j >= J ? 0 : 1)) & 1);
                 if (j >= J) {
-                    // past the last block: that block once more, which no one reads
-                    issue_one(j - J, min(kb + 2, k1 - 1), (kb - k0) & 1);
-                    if (j == kTiles - 1)
-#pragma unroll
-                        for (int q = kTiles - J; q < C::kLoads; ++q)
-                            issue_one(q, min(kb + 2, k1 - 1), (kb - k0) & 1);
                     if (j > J && (j - J) % 2 == 0) read_x(next, (j - J) / 2 - 1);
                     if (j == J)
 #pragma unroll
