@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 24;
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxExperts = 65535;
 constexpr uint32_t kPlanBits = FP8_PLAN_MASK | (0xFFu << W4A16_PLAN_PARAM_SHIFT);
 
@@ -53,45 +54,103 @@ w4a16_status_t check_weights(int64_t E, int64_t K, int64_t N) {
 
 }  // namespace
 
+namespace {
+
+// The tiled kernel's workgroup tiles, by cfg - 1: columns, rows, workgroups per CU
+// and the measured time of one step (a block of K) of a CU's workgroups, us.
+struct TileShape {
+    int bn, bm, per_cu;
+    double step_us;
+};
+constexpr TileShape kTiles[4] = {{256, 256, 1, 1.85}, {128, 128, 1, 0.76}, {64, 64, 2, 0.59},
+                                 {128, 64, 2, 0.83}};
+
+// Estimated time of a plan, us, from what the kernels were measured to do (256 CUs;
+// the constants describe a workgroup, so another count of CUs scales the rounds):
+//   launch and first loads 4; a tiled step as in kTiles, all workgroups of a CU
+//   together, in whole rounds; the loads to LDS 9.5 TB/s over the chip and the
+//   weights from HBM 5.2 TB/s, whichever takes longest; a split of K adds 2 and the
+//   last workgroup's reading of all partial tiles at 50 GB/s.
+double tiled_us(const TileShape& t, double tiles, int splits, int64_t KB, double rows,
+                double weight_bytes, int cus, bool grouped) {
+    const int64_t steps = (KB + splits - 1) / splits;
+    const double slots = (double)cus * t.per_cu;
+    const double rounds = __builtin_ceil(tiles * splits / slots);
+    // gathered rows of several experts share less of the L2: 2.2 us a step, measured
+    const double step = grouped && t.bn == 256 ? 2.2 : t.step_us;
+    double us = rounds * (double)steps * step;
+    const double live = rows < t.bm ? rows : t.bm;   // rows past the last repeat it
+    const double traffic = tiles * (double)KB * (t.bn + live) * kBlock / 9.5e6;
+    const double weights = weight_bytes / 5.2e6;
+    us = us < traffic ? traffic : us;
+    us = us < weights ? weights : us;
+    return us + 4.0 + (splits > 1 ? 2.0 + splits * (double)t.bn * t.bm * 4 / 50e3 : 0.0);
+}
+
+// The streaming kernel: rounds of two workgroups per CU, each 3.7 us and a share per
+// block of K that grows with the rows.
+double stream_us(double strips, int64_t KB, double rows, int cus) {
+    const double block = rows <= 8 ? 0.09 : rows <= 16 ? 0.15 : 0.18;
+    return __builtin_ceil(strips / (2.0 * cus)) * (3.7 + (double)KB * block);
+}
+
+}  // namespace
+
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int cus) {
-    // columns and rows of the tiled kernel's workgroup, by cfg - 1
-    static const int kBn[4] = {256, 128, 64, 64}, kBm[4] = {256, 128, 64, 128};
     Plan p{};
     const uint32_t hint = flags & FP8_PLAN_MASK;
     const int param = (int)((flags >> W4A16_PLAN_PARAM_SHIFT) & 0xFFu);
     const int64_t NB = (N + kBlock - 1) / kBlock;
     const int64_t KB = (K + kBlock - 1) / kBlock;
-    const int64_t per = E ? (M + E - 1) / E : M;   // rows an expert has, on average
-    p.splits = 1;
-    if (hint == FP8_PLAN_STREAM || (hint != FP8_PLAN_TILED && per <= 32)) {
+    const double rows = E ? (double)M / (double)E : (double)M;   // an expert's, on average
+    // experts with a row, if rows chose evenly
+    const double used = E ? (double)(M < E ? M : E) : 1.0;
+    const double weight_bytes = used * (double)K * (double)N;
+
+    double best = 1e30;
+    if (hint != FP8_PLAN_TILED) {
         p.variant = STREAM;
-        p.cfg = hint == FP8_PLAN_STREAM && (param == 1 || param == 2) ? param : per <= 16 ? 1 : 2;
+        p.cfg = hint == FP8_PLAN_STREAM && (param == 1 || param == 2) ? param : rows <= 16 ? 1 : 2;
         p.bn = 16;
         p.bm = 16 * p.cfg;
-        p.tiles = 0;
-        return p;
+        p.splits = 1;
+        if (hint == FP8_PLAN_STREAM) return p;
+        // more than 32 rows read the weights again for each 32
+        if (rows <= 32) best = stream_us(used * (double)(NB * kPanelTiles), KB, rows, cus);
     }
-    p.variant = TILED;
-    if (hint == FP8_PLAN_TILED && param >= 1 && param <= 4)
-        p.cfg = param;
-    else
-        p.cfg = per <= 64 ? 3 : per <= 128 ? 4 : per <= 512 ? 2 : 1;
-    p.bn = kBn[p.cfg - 1];
-    p.bm = kBm[p.cfg - 1];
-    const int64_t nbn = (NB * kBlock + p.bn - 1) / p.bn;
-    // grouped: each expert with rows may leave one tile unfilled
-    const int64_t nbm = E ? M / p.bm + (M < E ? M : E) : (M + p.bm - 1) / p.bm;
-    p.tiles = nbm * nbn;
-    if (!E && p.cfg > 1) {
-        // parts of K while a CU would be left without a workgroup, each of 4 blocks at least
-        while (p.splits < 8 && p.tiles * p.splits * 2 <= 2 * (int64_t)cus &&
-               KB >= 8 * p.splits && p.tiles <= (int64_t)(kCounterBytes / 4))
-            p.splits *= 2;
-        const int64_t part = (KB + p.splits - 1) / p.splits;
-        p.splits = (int)((KB + part - 1) / part);      // no empty part
-        if (p.splits > 1)
-            p.workspace = kCounterBytes + (size_t)p.tiles * p.splits * p.bn * p.bm * 4;
+    for (int c = 1; c <= 4; ++c) {
+        if (hint == FP8_PLAN_TILED && param >= 1 && param <= 4 && c != param) continue;
+        const TileShape& t = kTiles[c - 1];
+        const int64_t nbn = (NB * kBlock + t.bn - 1) / t.bn;
+        // grouped: each expert with rows may leave one tile unfilled, half of one on average
+        const int64_t nbm = E ? M / t.bm + (M < E ? M : E) : (M + t.bm - 1) / t.bm;
+        double mtiles = (double)nbm;
+        if (E) {
+            mtiles = (double)M / t.bm + used / 2;
+            mtiles = mtiles < used ? used : mtiles;
+        }
+        // no split for groups, nor for the 256 x 256 tile: its partial tiles cost more than
+        // they save (M = 1024, K = 8192, N = 28672: 1147 us with K in 4 parts, 227 whole)
+        int64_t most = E || c == 1 || nbm * nbn > (int64_t)(kCounterBytes / 4) ? 1 : KB / 4;
+        most = most > kMaxSplits ? kMaxSplits : most < 1 ? 1 : most;
+        for (int s = 1; s <= (int)most; ++s) {
+            const int64_t part = (KB + s - 1) / s;
+            if ((KB + part - 1) / part != s) continue;   // would leave a part empty
+            const double us = tiled_us(t, mtiles * (double)nbn, s, KB, rows, weight_bytes, cus,
+                                       E != 0);
+            if (us < best) {
+                best = us;
+                p.variant = TILED;
+                p.cfg = c;
+                p.bn = t.bn;
+                p.bm = t.bm;
+                p.tiles = nbm * nbn;
+                p.splits = s;
+            }
+        }
     }
+    if (p.variant == TILED && p.splits > 1)
+        p.workspace = kCounterBytes + (size_t)p.tiles * p.splits * p.bn * p.bm * 4;
     return p;
 }
 

@@ -49,21 +49,41 @@ __device__ __forceinline__ uint32_t to_half(float v) {
     return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// Four consecutive columns n .. n+3 of a row: one 8-byte store where rows are
-// 8-byte aligned (N % 4 == 0, and then n + 3 < N whenever n < N).
+// Consecutive columns n .. of a row in one store.  Rows of Y start at any even
+// address (N may be odd); global memory takes such stores whole, and at the end
+// of a row the columns go one by one.
+typedef int i32x2_row __attribute__((ext_vector_type(2), aligned(2)));
+typedef int i32x4_row __attribute__((ext_vector_type(4), aligned(2)));
+
+__device__ __forceinline__ int pack2(float a, float b) {
+    return (int)(to_half(a) | (to_half(b) << 16));
+}
+
 __device__ __forceinline__ void store4(void* Y, int64_t row, int n, int N, f32x4 v) {
     uint16_t* y = (uint16_t*)Y + row * N + n;
-    if ((N & 3) == 0) {
-        if (n < N) {
-            uint2 w;
-            w.x = to_half(v[0]) | (to_half(v[1]) << 16);
-            w.y = to_half(v[2]) | (to_half(v[3]) << 16);
-            *(uint2*)y = w;
-        }
+    if (n + 4 <= N) {
+        i32x2_row w;
+        w[0] = pack2(v[0], v[1]);
+        w[1] = pack2(v[2], v[3]);
+        *(i32x2_row*)y = w;
     } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (n + r < N) y[r] = (uint16_t)to_half(v[r]);
+    }
+}
+
+__device__ __forceinline__ void store8(void* Y, int64_t row, int n, int N, f32x4 lo, f32x4 hi) {
+    if (n + 8 <= N) {
+        i32x4_row w;
+        w[0] = pack2(lo[0], lo[1]);
+        w[1] = pack2(lo[2], lo[3]);
+        w[2] = pack2(hi[0], hi[1]);
+        w[3] = pack2(hi[2], hi[3]);
+        *(i32x4_row*)((uint16_t*)Y + row * N + n) = w;
+    } else {
+        store4(Y, row, n, N, lo);
+        store4(Y, row, n + 4, N, hi);
     }
 }
 
@@ -665,24 +685,11 @@ fp8_tiled_kernel(GemmArgs a) {
         if (m < rt.hi) {
             bool ok;
             x_row<GROUPED>(a, m, ok);
-            uint16_t* y = (uint16_t*)a.Y + (int64_t)m * a.N + n;
 #pragma unroll
             for (int i = 0; i < NT; i += 2) {
                 f32x4 lo = acc[i][t], hi = acc[i + 1][t];
                 if (!ok) lo = hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if ((a.N & 7) == 0) {   // rows and groups of 8 columns are 16-byte aligned
-                    if (n + 4 * i < a.N) {
-                        i32x4 v;
-                        v[0] = (int)(to_half(lo[0]) | (to_half(lo[1]) << 16));
-                        v[1] = (int)(to_half(lo[2]) | (to_half(lo[3]) << 16));
-                        v[2] = (int)(to_half(hi[0]) | (to_half(hi[1]) << 16));
-                        v[3] = (int)(to_half(hi[2]) | (to_half(hi[3]) << 16));
-                        *(i32x4*)(y + 4 * i) = v;
-                    }
-                } else {
-                    store4(a.Y, m, n + 4 * i, a.N, lo);
-                    store4(a.Y, m, n + 4 * i + 4, a.N, hi);
-                }
+                store8(a.Y, m, n + 4 * i, a.N, lo, hi);
             }
         }
     }
@@ -705,10 +712,10 @@ hipError_t launch_tiled_t(const GemmArgs& a, const Plan& p, hipStream_t stream) 
 
 hipError_t launch_tiled(const GemmArgs& a, const Plan& p, hipStream_t stream) {
     switch (p.cfg) {
-        case 1: return launch_tiled_t<2, 4, 8, 4, 2>(a, p, stream);   // 132 KiB of LDS
-        case 2: return launch_tiled_t<2, 2, 4, 4, 2>(a, p, stream);   // 66 KiB: two per CU
-        case 3: return launch_tiled_t<2, 2, 2, 2, 4>(a, p, stream);   // 68 KiB
-        default: return launch_tiled_t<2, 2, 2, 4, 3>(a, p, stream);  // 75 KiB
+        case 1: return launch_tiled_t<2, 4, 8, 4, 2>(a, p, stream);   // 130 KiB of LDS
+        case 2: return launch_tiled_t<2, 4, 4, 2, 4>(a, p, stream);   // 136 KiB
+        case 3: return launch_tiled_t<2, 2, 2, 2, 4>(a, p, stream);   // 68 KiB: two per CU
+        default: return launch_tiled_t<2, 2, 4, 2, 3>(a, p, stream);  // 75 KiB: two per CU
     }
 }
 
