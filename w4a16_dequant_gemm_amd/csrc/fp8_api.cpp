@@ -99,7 +99,7 @@ double stream_us(double strips, int64_t KB, double rows, int cus) {
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int cus) {
     Plan p{};
     const uint32_t hint = flags & FP8_PLAN_MASK;
-    const int param = (int)((flags >> W4A16_PLAN_PARAM_SHIFT) & 0xFFu);
+    int param = (int)((flags >> W4A16_PLAN_PARAM_SHIFT) & 0xFFu);
     const int64_t NB = (N + kBlock - 1) / kBlock;
     const int64_t KB = (K + kBlock - 1) / kBlock;
     const double rows = E ? (double)M / (double)E : (double)M;   // an expert's, on average
@@ -107,6 +107,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int c
     const double used = E ? (double)(M < E ? M : E) : 1.0;
     const double weight_bytes = used * (double)K * (double)N;
 
+    if (hint == FP8_PLAN_TILED && param == 1 && KB < 4) param = 0;   // its scales come by fours
     double best = 1e30;
     if (hint != FP8_PLAN_TILED) {
         p.variant = STREAM;
@@ -120,6 +121,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int c
     }
     for (int c = 1; c <= 4; ++c) {
         if (hint == FP8_PLAN_TILED && param >= 1 && param <= 4 && c != param) continue;
+        if (c == 1 && KB < 4) continue;
         const TileShape& t = kTiles[c - 1];
         const int64_t nbn = (NB * kBlock + t.bn - 1) / t.bn;
         // grouped: each expert with rows may leave one tile unfilled, half of one on average

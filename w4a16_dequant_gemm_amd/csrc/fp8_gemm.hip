@@ -360,11 +360,15 @@ struct Tile {
     static constexpr int BM = 16 * MT * WM;
     static constexpr int kWBytes = BN * kBlock;
     static constexpr int kXBytes = BM * kBlock;
-    static constexpr int kStage = kWBytes + kXBytes + 256 * kWaves;
+    // Two stages: the next step's operands are read ahead, and the scales come in
+    // groups of four blocks, outside the stages.
+    static constexpr bool kAhead = STAGES == 2;
+    static constexpr int kStage = kWBytes + kXBytes + (kAhead ? 0 : 256 * kWaves);
+    static constexpr int kGroup = kAhead ? 1024 * kWaves : 0;   // scales of four blocks
     static constexpr int kWLoads = BN / 8 / kWaves;   // 1-KiB loads of a wave per stage
     static constexpr int kXLoads = BM / 8 / kWaves;
     static constexpr int kLoads = kWLoads + kXLoads + 1;
-    static constexpr int kLds = STAGES * kStage;
+    static constexpr int kLds = STAGES * kStage + 2 * kGroup;
 };
 
 // The order of a wave's tiles within a step where the next step's operands are read
@@ -391,7 +395,7 @@ fp8_tiled_kernel(GemmArgs a) {
     using C = Tile<WN, WM, NT, MT, STAGES>;
     constexpr int BM = C::BM;
     constexpr int GM = 4;
-    constexpr bool AHEAD = STAGES == 2;
+    constexpr bool AHEAD = C::kAhead;
     static_assert(NT % 2 == 0 && NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
     static_assert(C::BM / 64 < C::kWaves, "a wave is left for the weights' scales");
     extern __shared__ __attribute__((aligned(128))) uint8_t lds[];
@@ -472,15 +476,20 @@ fp8_tiled_kernel(GemmArgs a) {
         uint8_t* st = lds + slot * C::kStage;
         uint8_t* xst = st + C::kWBytes;
         if (q < C::kWLoads) {
-            load16_to_lds(wsrc[q] + (size_t)kb * kChunkBytes + lane16,
+            load16_to_lds(wsrc[q] + (size_t)kb * kChunkBytes + fresh(lane16),
                           st + (wave * C::kWLoads + q) * 1024);
         } else if (q < C::kWLoads + C::kXLoads) {
             const int i = q - C::kWLoads;
             const uint8_t* src = a.xq + (size_t)kb * kBlock + ((size_t)fresh(xsrc[i]) << 4);
-            if (kb * kBlock + 16 * piece(lane, i) >= a.K) src = zero;
+            if (kb * kBlock + 16 * piece((int)fresh((uint32_t)lane), i) >= a.K) src = zero;
             load16_to_lds(src, xst + (wave * C::kXLoads + i) * 1024);
-        } else {
+        } else if constexpr (!AHEAD) {
             load4_to_lds((const uint8_t*)(sbase + kb) + ssrc, xst + C::kXBytes + wave * 256);
+        } else if ((kb & 3) == 0 && wave <= BM / 64) {
+            // four blocks at once: a row of scales is a line of its own, and 64 of them
+            // per load and step cost 4% (the last group starts early enough to end in the row)
+            load16_to_lds((const uint8_t*)(sbase + min(kb, KB - 4)) + fresh(ssrc),
+                          lds + STAGES * C::kStage + ((kb >> 2) & 1) * C::kGroup + wave * 1024);
         }
     };
     auto issue = [&](int kb, int slot) __attribute__((always_inline)) {
@@ -547,13 +556,34 @@ fp8_tiled_kernel(GemmArgs a) {
 #pragma unroll
         for (int q = 0; kEvery * q < kTiles - J; ++q)   // the others follow in the first step
             if (q < C::kLoads) issue_one(q, min(k0 + 1, k1 - 1), 1);
+        auto scales = [&](int kb, float (&v)[MT]) __attribute__((always_inline)) {
+            const uint8_t* g = lds + STAGES * C::kStage + ((kb >> 2) & 1) * C::kGroup +
+                               4 * (kb - min(kb & ~3, KB - 4));
+            const float sw = *(const float*)(g + 1024 * (BM / 64) + 16 * (wn * NT / kPanelTiles));
+            const uint8_t* x = g + 256 * wm * MT + 16 * (fresh((uint32_t)lane) & 15);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) v[t] = *(const float*)(x + 256 * t) * sw;
+        };
+        if (rt.lo + wm * MT * 16 >= rt.hi) {
+            // no row of the wave's is real: it only loads, and leaves the matrix unit to
+            // the wave it shares a SIMD with
+            for (int kb = k0; kb < k1; ++kb) {
+#pragma unroll
+                for (int q = 0; q < C::kLoads; ++q)
+                    if (kEvery * q >= kTiles - J) issue_one(q, min(kb + 1, k1 - 1), (kb - k0 + 1) & 1);
+                stage_barrier<0>();
+#pragma unroll
+                for (int q = 0; q < C::kLoads; ++q)
+                    if (kEvery * q < kTiles - J) issue_one(q, min(kb + 2, k1 - 1), (kb - k0) & 1);
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            return;
+        }
         w[0] = read_w(lds, 0);
         w[1] = read_w(lds, 1);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            read_x(lds, t);
-            s[t] = *(const float*)(lds + xsoff + 64 * t) * *(const float*)(lds + wsoff);
-        }
+        for (int t = 0; t < MT; ++t) read_x(lds, t);
+        scales(k0, s);
         for (int kb = k0; kb < k1; ++kb) {
             const uint8_t* st = lds + ((kb - k0) & 1) * C::kStage;
             const uint8_t* next = lds + ((kb - k0 + 1) & 1) * C::kStage;
@@ -577,11 +607,7 @@ fp8_tiled_kernel(GemmArgs a) {
                               min(kb + (j >= J ? 2 : 1), k1 - 1), (kb - k0 + (j >= J ? 0 : 1)) & 1);
                 if (j >= J) {
                     if (j > J && (j - J) % 2 == 0) read_x(next, (j - J) / 2 - 1);
-                    if (j == J)
-#pragma unroll
-                        for (int t = 0; t < MT; ++t)
-                            s_new[t] = *(const float*)(next + xsoff + 64 * t) *
-                                       *(const float*)(next + wsoff);
+                    if (j == J) scales(kb + 1, s_new);
                 }
                 const int l = j < kLag ? j - kLag + kTiles : j - kLag;
                 multiply(O::col(j), O::row(j), O::col(l), O::row(l),
@@ -698,7 +724,9 @@ fp8_tiled_kernel(GemmArgs a) {
 template <int WN, int WM, int NT, int MT, int STAGES>
 hipError_t launch_tiled_t(const GemmArgs& a, const Plan& p, hipStream_t stream) {
     using C = Tile<WN, WM, NT, MT, STAGES>;
-    if (p.bn != C::BN || p.bm != C::BM) return hipErrorInvalidValue;   // plan and kernel agree
+    // plan and kernel agree
+    if (p.bn != C::BN || p.bm != C::BM || (C::kAhead && (a.KB < 4 || a.splits > 1)))
+        return hipErrorInvalidValue;
     const int64_t grid = (p.tiles * p.splits + 7) / 8 * 8;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (a.offsets)
