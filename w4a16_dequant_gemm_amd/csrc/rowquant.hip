@@ -69,37 +69,40 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[kPiece]) {
     *((u32x4*)p + 1) = b;
 }
 
-// g / (1 + exp(-g)) through e = exp(-|g|) <= 1, which neither overflows nor
-// loses the quotient: 1 / (1 + e) lies in [1/2, 1].  exp2's argument is split
-// into a rounded product and its remainder (the low part of log2 e included),
-// so e is good to about two units in the last place over the whole range;
-// below exp(-87) e is 0, where the result is under 2^-119 |g|.
+// g / (1 + exp(-g)).  exp2's argument is split into a rounded product and its
+// remainder (the low part of log2 e included), so the exponential is good to about
+// one unit in the last place, and the quotient is the product with the reciprocal
+// corrected by its remainder: the instructions' own units (one each) would flip
+// codes next to a border.  Below -88, where the result is under 2^-119, g is taken
+// as -88; the exponent's argument stops at 128, where the exponential is 0.
 __device__ __forceinline__ float silu(float g) {
-    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-    const float m = fmaxf(-fabsf(g), -128.0f);   // e is 0 from there on; keeps l finite
+    constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
+    constexpr float kLowLn2 = 0x1.4ae0cp-26f * kLn2;   // the low part of log2 e, times ln 2
+    const float m = -__builtin_amdgcn_fmed3f(g, -88.0f, 128.0f);
+    g = __builtin_amdgcn_fmed3f(g, -88.0f, 0x1.fffffep+127f);
     const float h = m * kLog2e;
-    const float l = __builtin_fmaf(m, kLog2eLow, __builtin_fmaf(m, kLog2e, -h));
+    const float l = __builtin_fmaf(__builtin_fmaf(m, kLog2e, -h), kLn2, m * kLowLn2);
     float e = __builtin_amdgcn_exp2f(h);
-    e = __builtin_fmaf(e, l * kLn2, e);
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    return g * (g >= 0.0f ? r : e * r);
+    e = __builtin_fmaf(e, l, e);
+    const float d = 1.0f + e;
+    const float r = __builtin_amdgcn_rcpf(d);
+    const float q = g * r;
+    return __builtin_fmaf(__builtin_fmaf(-d, q, g), r, q);
 }
 
-__device__ __forceinline__ float clamp448(float v) {
-    return __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f);
-}
-
-// 16 values times r as E4M3 codes; v_cvt_pk_fp8_f32 rounds to nearest even.
+// 16 values times r as E4M3 codes; v_cvt_pk_fp8_f32 rounds to nearest even.  SAT:
+// values may lie above 464, which would not round to 448 any more.
+template <bool SAT>
 __device__ __forceinline__ u32x4 codes16(const float (&v)[kPiece], float r) {
+    float t[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+        t[i] = SAT ? __builtin_amdgcn_fmed3f(v[i] * r, -448.0f, 448.0f) : v[i] * r;
     u32x4 q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * i] * r), clamp448(v[4 * i + 1] * r), w,
-                                            false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(v[4 * i + 2] * r), clamp448(v[4 * i + 3] * r),
-                                            w, true);
-        q[i] = (uint32_t)w;
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * i], t[4 * i + 1], 0, false);
+        q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * i + 2], t[4 * i + 3], w, true);
     }
     return q;
 }
@@ -162,7 +165,7 @@ __device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_
         a = fmaxf(a, __shfl_xor(a, 2, 64));
         a = fmaxf(a, __shfl_xor(a, 4, 64));
         a = fmaxf(a, kTinyMax);
-        const u32x4 w = codes16(v, __fdiv_rn(448.0f, a));
+        const u32x4 w = codes16<false>(v, __fdiv_rn(448.0f, a));   // up to 448 and a rounding
         if (live) {
             *(u32x4*)((uint8_t*)q + at) = w;
             if ((piece & 7) == 0) ((float*)s)[block] = __fdiv_rn(a, 448.0f);
@@ -172,7 +175,7 @@ __device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_
         a = fmaxf(a, __shfl_xor(a, 1, 64));
         const int ef = (int)(__float_as_uint(a) >> 23);                 // a >= 0
         const int E = max(ef - 127 - 8, -127);   // floor(log2 a) - 8; subnormal a: -127 as well
-        const u32x4 w = codes16(v, __uint_as_float((uint32_t)(127 - E) << 23));
+        const u32x4 w = codes16<true>(v, __uint_as_float((uint32_t)(127 - E) << 23));
         if (live) {
             *(u32x4*)((uint8_t*)q + at) = w;
             if ((piece & 1) == 0) ((uint8_t*)s)[at / 32] = (uint8_t)(E + 127);
@@ -278,7 +281,8 @@ __global__ __launch_bounds__(kFlatThreads) void swiglu_flat_kernel(RowArgs a) {
     const int64_t idx = (int64_t)blockIdx.x * kFlatThreads + threadIdx.x;
     const int64_t item = idx >> 3;
     const int64_t items = a.T * a.KB;
-    const int64_t row = items >> 32 ? item / a.KB : (int64_t)((uint32_t)item / (uint32_t)a.KB);
+    const int64_t row = items >> 31 ? item / a.KB
+                                    : (int64_t)(((uint64_t)(uint32_t)item * a.kb_magic) >> a.kb_shift);
     const int64_t block = item - row * a.KB;
     const int64_t piece = block * 8 + (idx & 7);
     const bool live = item < items && piece < a.W / kPiece;

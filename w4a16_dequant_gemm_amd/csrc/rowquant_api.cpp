@@ -56,7 +56,7 @@ w4a16_status_t rowquant_rmsnorm(const void* x, int64_t ldx, const void* residual
     if (!x || !weight || !aligned16(x) || !aligned16(residual) || !aligned16(weight) ||
         !aligned16(h_out) || !out_ok(q, s, kind))
         return W4A16_ERR_INVALID_ARG;
-    const RowArgs a{x, residual, weight, h_out, q, s, ldx, ldr, T, W, (W + 127) / 128, eps};
+    const RowArgs a{x, residual, weight, h_out, q, s, ldx, ldr, T, W, (W + 127) / 128, eps, 0, 0};
     return from_hip((flags & ROWQUANT_IN_BF16) ? launch_norm_bf16(a, kind, (hipStream_t)stream)
                                                : launch_norm_f16(a, kind, (hipStream_t)stream));
 }
@@ -70,7 +70,8 @@ w4a16_status_t rowquant_swiglu(const void* gate, int64_t ldg, const void* up, in
     if (T == 0) return W4A16_OK;
     if (!gate || !up || !aligned16(gate) || !aligned16(up) || !out_ok(q, s, kind))
         return W4A16_ERR_INVALID_ARG;
-    const RowArgs a{gate, up, nullptr, nullptr, q, s, ldg, ldu, T, W, (W + 127) / 128, 0.0f};
+    RowArgs a{gate, up, nullptr, nullptr, q, s, ldg, ldu, T, W, (W + 127) / 128, 0.0f, 0, 0};
+    set_division(a);
     return from_hip((flags & ROWQUANT_IN_BF16) ? launch_swiglu_bf16(a, kind, (hipStream_t)stream)
                                                : launch_swiglu_f16(a, kind, (hipStream_t)stream));
 }
