@@ -140,3 +140,27 @@ def test_plan_hint_names(lib):
     assert fp8.plan_flags_fp8(("tiled", 2)) == 0x20 | (2 << 8)
     with pytest.raises(ValueError):
         fp8.plan_flags_fp8("decode")
+
+
+def test_limits(lib):
+    """The largest row counts and X the kernels' 32-bit counting takes are refused beyond."""
+    big = (1 << 30) + 1
+    assert lib.fp8_gemm(FAKE, FAKE, FAKE, 1 << 40, FAKE, big, 16, 16, 0, FAKE, 1 << 40, None) == INV
+    assert lib.fp8_gemm(FAKE, FAKE, FAKE, 1 << 40, FAKE, 1 << 20, 16, 1 << 17, 0, FAKE, 1 << 40,
+                        None) == INV                        # X of 2^37 bytes
+    assert lib.fp8_grouped_gemm(FAKE, FAKE, FAKE, 1 << 40, FAKE, FAKE, FAKE, 8, big, 3, 256, 512, 0,
+                                None) == INV
+    assert lib.fp8_grouped_gemm(FAKE, FAKE, FAKE, 1 << 40, FAKE, FAKE, FAKE, big, 8, 3, 256, 512, 0,
+                                None) == INV
+
+
+@pytest.mark.parametrize("K", [16, 128, 384, 512, 4096, 8208])
+def test_workspace_follows_the_plan(lib, K):
+    """A hint for the 256 x 256 tile never splits K (nor is taken below four blocks), and a
+    split's workspace holds its counters and whole partial tiles."""
+    from w4a16_dequant_gemm_amd import fp8
+    one = fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8(("tiled", 1)))
+    assert one == 0 or K < 512
+    assert fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8("stream")) == 0
+    small = fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8(("tiled", 3)))
+    assert small == 0 or (small - 65536) % (2 * 8 * 64 * 64 * 4) == 0

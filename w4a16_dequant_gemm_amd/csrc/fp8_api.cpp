@@ -14,7 +14,7 @@ namespace fp8 {
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 24;
-constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxRows = ((int64_t)1 << 30) + 1;   // row counts fit int with a tile to spare
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxExperts = 65535;
 constexpr uint32_t kPlanBits = FP8_PLAN_MASK | (0xFFu << W4A16_PLAN_PARAM_SHIFT);

@@ -424,6 +424,7 @@ fp8_tiled_kernel(GemmArgs a) {
     RowTile rt{0, 0, 0};
     if constexpr (GROUPED) {
         rt = find_row_tile<BM>(a, mb, lane);
+        if (rt.lo >= rt.hi) return;   // offsets that do not ascend
     } else {
         rt.lo = mb * BM;
         rt.hi = (int)min((int64_t)rt.lo + BM, a.M);
