@@ -394,7 +394,9 @@ __global__ __launch_bounds__(WN* WM * 64) __attribute__((amdgpu_waves_per_eu(2, 
 fp8_tiled_kernel(GemmArgs a) {
     using C = Tile<WN, WM, NT, MT, STAGES>;
     constexpr int BM = C::BM;
-    constexpr int GM = 4;
+    // row tiles by all column tiles in turn (us, GM = 2, 4, 8, 16 in one job: 4096 rows
+    // K = 8192 N = 28672 845, 834, 840, 855; 16384 rows over 16 experts 660, 631, 612, 618)
+    constexpr int GM = GROUPED ? 8 : 4;
     constexpr bool AHEAD = C::kAhead;
     static_assert(NT % 2 == 0 && NT <= kPanelTiles && C::kWLoads >= 1 && C::kXLoads >= 1 && STAGES >= 2, "shape");
     static_assert(C::BM / 64 < C::kWaves, "a wave is left for the weights' scales");
