@@ -62,7 +62,7 @@ struct Plan {
     Variant variant;
     int cfg;         // STREAM: row tiles of 16 (1, 2); TILED: workgroup tile, see launch_tiled
     int bn, bm;      // columns and rows of a workgroup
-    int splits;      // TILED, one product: parts of K
+    int splits;      // TILED, one product, not the 256 x 256 tile: parts of K
     int64_t tiles;   // TILED: workgroup tiles (for groups: the most there can be)
     size_t workspace;
 };

@@ -6,7 +6,10 @@
 // are bound by HBM: a lane holds 16 consecutive elements (two 16-byte loads
 // per input, one 16-byte store of codes), so a block of 128 columns is 8
 // neighbouring lanes and an MX block of 32 is 2, and every block maximum is a
-// few lane shuffles.
+// few lane shuffles.  4096 rows: the norm with residual of 8192 columns 44 us (5.3
+// TB/s), the gated activation of 28672 columns 101-107 us (5.5-5.9 TB/s; its arithmetic,
+// 30 instructions an element, takes about as long as its bytes), both to fp8; a
+// device copy reaches 5.1.  One row of 4096: 2.4 us.
 //
 // Compiled once per input dtype (ROWQUANT_TU_BF16 = 0 fp16, 1 bf16).
 #include <hip/hip_runtime.h>
@@ -125,8 +128,8 @@ __device__ __forceinline__ RowScale int8_scale(float amax) {
 }
 
 // v / s rounded once: the product with the correctly rounded reciprocal,
-// corrected by its exact remainder, then half to even to an integer.  A scale
-// so small that its reciprocal overflows takes the division itself.
+// corrected by its exact remainder, then half to even to an integer (emit divides
+// where the scale is so small that its reciprocal overflows).
 __device__ __forceinline__ uint32_t int8_code(float v, RowScale rs) {
     float t = v * rs.inv;
     t = __builtin_fmaf(__builtin_fmaf(-t, rs.s, v), rs.inv, t);
@@ -136,7 +139,7 @@ __device__ __forceinline__ uint32_t int8_code(float v, RowScale rs) {
 
 // Quantise and store one piece.  Every lane of the wave takes part (the block
 // maxima are shuffles); only live ones store.  at: index of the piece's first
-// element in q; block: index of its 128-block's scale; W: the row length.
+// element in q; block: index of its 128-block's scale; piece: its place in the row.
 template <int KIND>
 __device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_t at,
                                      int64_t block, int piece, void* q, void* s, RowScale rs) {
