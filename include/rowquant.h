@@ -50,7 +50,7 @@ extern "C" {
  *   x         dev, [T] rows of W elements, ldx apart;  residual the same with ldr;
  *   weight    dev, [W];  h_out  dev, [T][W] in the inputs' dtype, h rounded once
  *             (NULL: not wanted; it may be x or residual if those are contiguous).
- *   W <= ROWQUANT_MAX_ROW, eps >= 0.
+ *   W <= ROWQUANT_MAX_ROW, eps >= 0 (with eps = 0 a row of zeros has no norm).
  */
 w4a16_status_t rowquant_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr,
                                 const void *weight, float eps, void *h_out, void *q, void *s,
