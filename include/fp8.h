@@ -43,7 +43,8 @@ extern "C" {
 #define FP8_BF16 0x1u
 /* Plan hints (tests and benchmarks).  W4A16_PLAN_PARAM(n): the streaming
  * kernel's row tiles of 16 (1 or 2), or the tiled kernel's workgroup tile
- * (columns x rows; 1: 256 x 256, 2: 128 x 128, 3: 64 x 64, 4: 128 x 64).  A
+ * (columns x rows; 1: 256 x 256, 2: 128 x 128, 3: 64 x 64, 4: 128 x 64,
+ * 5: 256 x 64, 6: 128 x 64 with more stages).  A
  * hint that does not apply is ignored. */
 #define FP8_PLAN_STREAM 0x10u
 #define FP8_PLAN_TILED  0x20u

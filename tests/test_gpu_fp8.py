@@ -19,7 +19,8 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 E4M3 = torch.float8_e4m3fn
 DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
-PLANS = [None, ("stream", 1), ("stream", 2), ("tiled", 1), ("tiled", 2), ("tiled", 3), ("tiled", 4)]
+PLANS = [None, ("stream", 1), ("stream", 2), ("tiled", 1), ("tiled", 2), ("tiled", 3), ("tiled", 4),
+         ("tiled", 5), ("tiled", 6)]
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "../../include/fp8.h"
 #include "fp8_internal.h"
@@ -57,41 +58,60 @@ w4a16_status_t check_weights(int64_t E, int64_t K, int64_t N) {
 namespace {
 
 // The tiled kernel's workgroup tiles, by cfg - 1: columns, rows, workgroups per CU
-// and the measured time of one step (a block of K) of a CU's workgroups, us.
+// and the measured time of one step (a block of K) of a CU's workgroups, us, for one
+// product and for groups (whose weights come from HBM and whose rows share less of the
+// L2).  128 x 64 with six stages, one workgroup per CU, hides the loads of a layer
+// that is read once (16 rows, K = 8192, N = 28672: 43 us; 48 with 64 x 64, 52 with
+// three stages); with three stages and two workgroups per CU it hides the start and end of
+// short tiles (groups, K = 2048, 64 rows: 34 against 38).
 struct TileShape {
     int bn, bm, per_cu;
-    double step_us;
+    double step_us, grouped_us;
 };
-constexpr TileShape kTiles[4] = {{256, 256, 1, 1.85}, {128, 128, 1, 0.76}, {64, 64, 2, 0.59},
-                                 {128, 64, 2, 0.83}};
+constexpr int kTileShapes = 6;
+constexpr TileShape kTiles[kTileShapes] = {
+    {256, 256, 1, 1.78, 2.2}, {128, 128, 1, 0.71, 0.80}, {64, 64, 2, 0.59, 0.70},
+    {128, 64, 2, 0.83, 1.15}, {256, 64, 1, 1.05, 1.05},  {128, 64, 1, 0.57, 0.62}};
 
-// Estimated time of a plan, us, from what the kernels were measured to do (256 CUs;
-// the constants describe a workgroup, so another count of CUs scales the rounds):
-//   launch and first loads 4; a tiled step as in kTiles, all workgroups of a CU
-//   together, in whole rounds; the loads to LDS 9.5 TB/s over the chip and the
-//   weights from HBM 5.2 TB/s, whichever takes longest; a split of K adds 2 and the
-//   last workgroup's reading of all partial tiles at 50 GB/s.
-double tiled_us(const TileShape& t, double tiles, int splits, int64_t KB, double rows,
-                double weight_bytes, int cus, bool grouped) {
-    const int64_t steps = (KB + splits - 1) / splits;
-    const double slots = (double)cus * t.per_cu;
-    const double rounds = __builtin_ceil(tiles * splits / slots);
-    // gathered rows of several experts share less of the L2: 2.2 us a step, measured
-    const double step = grouped && t.bn == 256 ? 2.2 : t.step_us;
-    double us = rounds * (double)steps * step;
-    const double live = rows < t.bm ? rows : t.bm;   // rows past the last repeat it
-    const double traffic = tiles * (double)KB * (t.bn + live) * kBlock / 9.5e6;
-    const double weights = weight_bytes / 5.2e6;
-    us = us < traffic ? traffic : us;
-    us = us < weights ? weights : us;
-    return us + 4.0 + (splits > 1 ? 2.0 + splits * (double)t.bn * t.bm * 4 / 50e3 : 0.0);
+// The longest of what a plan has to do, and a tenth of the rest.
+double together(double a, double b, double c) {
+    const double most = a > b ? (a > c ? a : c) : (b > c ? b : c);
+    return most + 0.1 * (a + b + c - most);
 }
 
-// The streaming kernel: rounds of two workgroups per CU, each 3.7 us and a share per
-// block of K that grows with the rows.
-double stream_us(double strips, int64_t KB, double rows, int cus) {
+// Estimated time of a plan, us, from what the kernels were measured to do on 256 CUs:
+//   launch and first loads 4; rounds of workgroups (whole ones for one product; for
+//   groups, whose tiles are not known, a third of a round more than the average) of tiled steps, and 3 a round where a CU has
+//   no second workgroup to hide a tile's start and end; the loads to LDS at 12 TB/s
+//   over the chip; the weights from HBM at 5.2 TB/s; a split of K adds 4 and the last
+//   workgroup's reading of all partial tiles at 50 GB/s.
+double tiled_us(const TileShape& t, double tiles, int splits, int64_t KB, double rows,
+                double weight_bytes, int cus, bool grouped) {
+    const double steps = (double)((KB + splits - 1) / splits);
+    double rounds = tiles * splits / ((double)cus * t.per_cu);
+    rounds = grouped ? (rounds < 0.85 ? 1 : rounds + 0.3) : __builtin_ceil(rounds);
+    // a CU with one workgroup where two would fit steps faster
+    const bool alone = grouped && t.per_cu == 2 && tiles < 0.5 * cus * t.per_cu;
+    const double compute = rounds * (steps * (grouped ? t.grouped_us : t.step_us) *
+                                         (alone ? 0.6 : 1.0) +
+                                     (t.per_cu == 1 ? 3.0 : 0.0));
+    const double live = rows < t.bm ? rows : t.bm;   // rows past the last repeat it
+    const double traffic = tiles * (double)KB * (t.bn + live) * kBlock / 12e6;
+    return together(compute, traffic, weight_bytes / 5.2e6) + 4.0 +
+           (splits > 1 ? 4.0 + splits * (double)t.bn * t.bm * 4 / 50e3 : 0.0);
+}
+
+// The streaming kernel: rounds of two workgroups per CU, each with a start and end and
+// a share per block of K that grows with the rows; every strip reads the rows again, at
+// 9.5 TB/s.
+double stream_us(double strips, int64_t KB, double rows, double weight_bytes, int cus,
+                 bool grouped) {
+    const double rounds = strips / (2.0 * cus);
     const double block = rows <= 8 ? 0.09 : rows <= 16 ? 0.15 : 0.18;
-    return __builtin_ceil(strips / (2.0 * cus)) * (3.7 + (double)KB * block);
+    const double compute = grouped ? 4.0 + rounds * (3.2 + (double)KB * (block - 0.015))
+                                   : __builtin_ceil(rounds) * (3.7 + (double)KB * block);
+    const double traffic = strips * (double)KB * (16 + rows) * kBlock / 9.5e6;
+    return together(compute, traffic, weight_bytes / 5.2e6) + 2.0;
 }
 
 }  // namespace
@@ -104,7 +124,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int c
     const int64_t KB = (K + kBlock - 1) / kBlock;
     const double rows = E ? (double)M / (double)E : (double)M;   // an expert's, on average
     // experts with a row, if rows chose evenly
-    const double used = E ? (double)(M < E ? M : E) : 1.0;
+    const double used = E ? (double)E * (1.0 - std::exp(-rows)) : 1.0;
     const double weight_bytes = used * (double)K * (double)N;
 
     if (hint == FP8_PLAN_TILED && param == 1 && KB < 4) param = 0;   // its scales come by fours
@@ -117,10 +137,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int c
         p.splits = 1;
         if (hint == FP8_PLAN_STREAM) return p;
         // more than 32 rows read the weights again for each 32
-        if (rows <= 32) best = stream_us(used * (double)(NB * kPanelTiles), KB, rows, cus);
+        if (rows <= 32)
+            best = stream_us(used * (double)(NB * kPanelTiles), KB, rows, weight_bytes, cus,
+                             E != 0);
     }
-    for (int c = 1; c <= 4; ++c) {
-        if (hint == FP8_PLAN_TILED && param >= 1 && param <= 4 && c != param) continue;
+    for (int c = 1; c <= kTileShapes; ++c) {
+        if (hint == FP8_PLAN_TILED && param >= 1 && param <= kTileShapes && c != param) continue;
         if (c == 1 && KB < 4) continue;
         const TileShape& t = kTiles[c - 1];
         const int64_t nbn = (NB * kBlock + t.bn - 1) / t.bn;

@@ -770,7 +770,9 @@ hipError_t launch_tiled(const GemmArgs& a, const Plan& p, hipStream_t stream) {
         case 1: return launch_tiled_t<2, 4, 8, 4, 2>(a, p, stream);   // 130 KiB of LDS
         case 2: return launch_tiled_t<2, 4, 4, 2, 4>(a, p, stream);   // 136 KiB
         case 3: return launch_tiled_t<2, 2, 2, 2, 4>(a, p, stream);   // 68 KiB: two per CU
-        default: return launch_tiled_t<2, 2, 4, 2, 3>(a, p, stream);  // 75 KiB: two per CU
+        case 4: return launch_tiled_t<2, 2, 4, 2, 3>(a, p, stream);  // 75 KiB: two per CU
+        case 5: return launch_tiled_t<4, 2, 4, 2, 3>(a, p, stream);  // 126 KiB
+        default: return launch_tiled_t<4, 2, 2, 2, 6>(a, p, stream); // 156 KiB
     }
 }
 
