@@ -1,0 +1,60 @@
+"""GPU tests of calls with `stream=`: a call on another stream than torch's current one owes
+nothing to what the current stream still has to do."""
+import pytest
+
+from gpu_helpers import lib, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    lib()
+
+
+def f8():
+    from w4a16_dequant_gemm_amd import fp8
+    return fp8
+
+
+def whole_numbers(M, K, N, seed):
+    """An fp8 product whose result is exact: (xq, xs, packed, Y in bf16)."""
+    g = torch.Generator().manual_seed(seed)
+    xq, w = (torch.randint(-2, 3, (n, K), generator=g).float() for n in (M, N))
+    kb, nb = -(-K // 128), -(-N // 128)
+    xs, ws = torch.full((M, kb), 0.5), torch.full((nb, kb), 0.25)
+    want = (xq.double() @ w.double().t() * 0.125).to(torch.bfloat16).cuda()
+    packed = f8().fp8_repack(w.to(E4M3).cuda(), ws.cuda())
+    return xq.to(E4M3).cuda(), xs.cuda(), packed, want
+
+
+def keep_busy(x):
+    """Some tens of milliseconds of work for the current stream."""
+    for _ in range(30):
+        x = x @ x * 1e-3
+    return x
+
+
+def test_first_use_of_a_stream_whose_plan_needs_a_workspace():
+    xq, xs, packed, want = whole_numbers(100, 4096, 512, 1)
+    assert f8().fp8_workspace_bytes(100, 512, 4096) > 0      # K in parts
+    big = torch.rand(4096, 4096, device="cuda")
+    keep_busy(big)
+    for rep in range(3):
+        say(f"stream= with the current stream at work, {rep}")
+        side = torch.cuda.Stream()
+        Y = torch.full_like(want, float("nan"))
+        torch.cuda.synchronize()
+        keep_busy(big)
+        f8().fp8_gemm(xq, xs, packed, Y=Y, stream=side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            got = Y.clone()
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

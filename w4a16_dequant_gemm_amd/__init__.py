@@ -148,6 +148,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(_stream_handle(stream))
 
 
+def _on_stream(device_index: int, handle: int):
+    """Context in which torch allocates and fills for the hipStream_t `handle`."""
+    # a handle of 0 is the default stream; ExternalStream would take it for "any"
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device_index) if handle
+                             else torch.cuda.default_stream(device_index))
+
+
 def _bad(where: str):
     raise W4A16Error(W4A16_ERR_INVALID_ARG, where)
 
@@ -279,7 +286,9 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
         size *= 2
     if ws is not None:
         _retired_workspaces.append(ws)
-    ws = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", device_index))
+    # filled on the stream of the calls that will use it: nothing else orders the two
+    with _on_stream(device_index, stream_handle):
+        ws = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", device_index))
     _workspaces[key] = ws
     return ws
 
