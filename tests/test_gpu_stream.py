@@ -58,3 +58,33 @@ def test_first_use_of_a_stream_whose_plan_needs_a_workspace():
         side.synchronize()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_rows_dropped_in_a_chain_on_another_stream():
+    """The chain's rows are dropped while the other stream still reads them; the current
+    stream then makes and fills memory of the same sizes."""
+    from w4a16_dequant_gemm_amd import rowquant
+    T, K, N = 512, 4096, 1024
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(T, K, generator=g).to(torch.bfloat16).cuda()
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    _, _, packed, _ = whole_numbers(1, K, N, 3)
+    q, s, _ = rowquant.rmsnorm_quantize_rows(x, w)
+    want = f8().fp8_gemm(q, s, packed)
+    del q, s
+    big = torch.rand(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for rep in range(5):
+        say(f"chain on another stream, {rep}")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            keep_busy(big)
+        q, s, _ = rowquant.rmsnorm_quantize_rows(x, w, stream=side)
+        Y = f8().fp8_gemm(q, s, packed, stream=side)
+        shape = q.shape
+        del q, s
+        junk = [torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
+        del junk

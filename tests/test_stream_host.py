@@ -19,6 +19,8 @@ class Streams:
                             lambda handle, device=None: ("external", handle, device))
         monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", 0, device))
         monkeypatch.setattr(torch.cuda, "stream", self.use)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.stack[-1])
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: self.stack[-1])
         zeros = torch.zeros
 
         def noted(*shape, dtype=None, device=None):
@@ -47,3 +49,105 @@ def test_workspace_is_filled_on_the_stream_that_uses_it(streams, handle):
     assert w4._workspace_at(1 << 20, 0, handle) is ws
     w4._workspace_at((1 << 20) + 1, 0, handle)        # grows
     assert streams.made == [("zeros", handle)] * 2
+
+
+class FakeLibrary:
+    """Takes every call and launches nothing."""
+    def __getattr__(self, name):
+        return lambda *args: (1 << 20) if name.endswith("_packed_bytes") else 0
+
+
+class FakeTensor:
+    """What the binding asks of a contiguous tensor on device 0."""
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def __init__(self, *shape, dtype, recorded=None):
+        self.shape, self.dtype, self.recorded = torch.Size(shape), dtype, recorded
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self, i):
+        return self.shape[i + 1:].numel()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 0x10000
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+def fake(*shape, dtype):
+    return FakeTensor(*shape, dtype=dtype)
+
+
+def calls():
+    """name -> (a call with `stream=`, how many outputs it makes)."""
+    from w4a16_dequant_gemm_amd import fp8, mxfp4, rowquant, w4a8
+    half, u8, f32, i8, i32 = (torch.float16, torch.uint8, torch.float32, torch.int8, torch.int32)
+    x, w = fake(4, 512, dtype=half), fake(512, dtype=half)
+    rows = fake(4, 512, dtype=u8)
+    blob = fake(1 << 20, dtype=u8)
+    p16 = w4.PackedW4(blob, 512, 128, 128, 0, w4._layout_version)
+    p8 = w4a8.PackedW8(blob, 512, 128, 128)
+    one, many = (fp8.PackedFP8(blob, 1, 512, 128, g) for g in (False, True))
+    xs, off = fake(4, 4, dtype=f32), fake(2, dtype=i32)
+    return {
+        "norm": (lambda s: rowquant.rmsnorm_quantize_rows(x, w, residual=x, stream=s), 3),
+        "swiglu": (lambda s: rowquant.swiglu_quantize_rows(x, x, stream=s), 2),
+        "fp8_gemm": (lambda s: fp8.fp8_gemm(rows, xs, one, stream=s), 1),
+        "fp8_grouped_gemm": (lambda s: fp8.fp8_grouped_gemm(rows, xs, many, off, stream=s), 1),
+        "fp8_repack": (lambda s: fp8.fp8_repack(fake(128, 512, dtype=u8), fake(1, 4, dtype=f32),
+                                                stream=s), 1),
+        "w4a16_gemm": (lambda s: w4.w4a16_gemm(x, p16, stream=s), 1),
+        "w4a16_gemm_ex": (lambda s: w4.w4a16_gemm_ex(x, p16, stream=s), 1),
+        "w4a16_dequant": (lambda s: w4.w4a16_dequant(p16, stream=s), 1),
+        "w4a16_unrepack": (lambda s: w4.w4a16_unrepack(p16, stream=s), 3),
+        "w4a8_quantize_rows": (lambda s: w4a8.w4a8_quantize_rows(x, stream=s), 2),
+        "w4a8_gemm": (lambda s: w4a8.w4a8_gemm(fake(4, 512, dtype=i8), fake(4, dtype=f32), p8,
+                                               stream=s), 1),
+        "w4a8_dequant": (lambda s: w4a8.w4a8_dequant(p8, stream=s), 1),
+        "mxfp4_quantize_rows": (lambda s: mxfp4.mxfp4_quantize_rows(x, stream=s), 2),
+        "mxfp4_gemm": (lambda s: mxfp4.mxfp4_gemm(rows, fake(4, 16, dtype=u8),
+                                                  mxfp4.PackedMX(blob, 512, 128), stream=s), 1),
+    }
+
+
+NAMES = ["norm", "swiglu", "fp8_gemm", "fp8_grouped_gemm", "fp8_repack", "w4a16_gemm",
+         "w4a16_gemm_ex", "w4a16_dequant", "w4a16_unrepack", "w4a8_quantize_rows", "w4a8_gemm",
+         "w4a8_dequant", "mxfp4_quantize_rows", "mxfp4_gemm"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("handle", [CURRENT, 0x20, 0])
+def test_outputs_are_made_on_the_stream_of_the_call(streams, monkeypatch, name, handle):
+    """... and wait for torch's current stream too when they are dropped."""
+    from w4a16_dequant_gemm_amd import fp8, mxfp4, rowquant, w4a8
+    call, outputs = calls()[name]
+    made, recorded = [], []
+
+    def empty(shape, dtype=None, device=None):
+        made.append(streams.stack[-1])
+        return FakeTensor(*((shape,) if isinstance(shape, int) else shape), dtype=dtype,
+                          recorded=recorded)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "empty_like", lambda like, dtype=None:
+                        empty(like.shape, dtype=dtype or like.dtype))
+    monkeypatch.setattr(w4, "_lib", FakeLibrary())
+    for module in (fp8, rowquant, w4a8, mxfp4):
+        monkeypatch.setattr(module, "_lib", FakeLibrary)
+    monkeypatch.setattr(fp8, "_ws_bytes", {})
+    monkeypatch.setattr(w4, "_ws_bytes", {})
+    call(handle)
+    assert made == [handle] * outputs
+    assert recorded == ([] if handle == CURRENT else [CURRENT] * outputs)

@@ -155,6 +155,22 @@ def _on_stream(device_index: int, handle: int):
                              else torch.cuda.default_stream(device_index))
 
 
+def _empty_on(stream, shape, dtype, device: torch.device) -> torch.Tensor:
+    """An output of a call on `stream`.  It is made there, so that no kernel still under way
+    on torch's current stream holds the memory, and when it is dropped the memory waits for
+    both streams."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    handle = _stream_handle(stream)
+    if torch._C._cuda_getCurrentRawStream(index) == handle:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(index, handle):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
 def _bad(where: str):
     raise W4A16Error(W4A16_ERR_INVALID_ARG, where)
 
@@ -238,7 +254,7 @@ def w4a16_repack(qweight: torch.Tensor, scales: torch.Tensor, zeros: Optional[to
             _bad("w4a16_repack: the symmetric format takes no zeros")
     else:
         _require(zeros, "w4a16_repack: zeros", torch.uint8, (K // group_size) * N, dev)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    packed = _empty_on(stream, nbytes, torch.uint8, dev)
     _check(load_library().w4a16_repack(_ptr(qweight), _ptr(scales), _ptr(zeros), K, N,
                                        group_size, flags, _ptr(packed), nbytes, _stream(stream)),
            "w4a16_repack")
@@ -248,9 +264,9 @@ def w4a16_repack(qweight: torch.Tensor, scales: torch.Tensor, zeros: Optional[to
 def w4a16_unrepack(packed: PackedW4, stream=None):
     dev = packed.data.device
     K, N, G, flags = packed.K, packed.N, packed.group_size, packed.flags
-    qweight = torch.empty((K // 8, N), dtype=torch.int32, device=dev)
-    scales = torch.empty((K // G, N), dtype=torch_dtype(flags), device=dev)
-    zeros = None if flags & W4A16_SYM else torch.empty((K // G, N), dtype=torch.uint8, device=dev)
+    qweight = _empty_on(stream, (K // 8, N), torch.int32, dev)
+    scales = _empty_on(stream, (K // G, N), torch_dtype(flags), dev)
+    zeros = None if flags & W4A16_SYM else _empty_on(stream, (K // G, N), torch.uint8, dev)
     _check(load_library().w4a16_unrepack(_ptr(packed.data), packed.data.numel(), _ptr(qweight),
                                          _ptr(scales), _ptr(zeros), K, N, G, flags,
                                          _stream(stream)), "w4a16_unrepack")
@@ -296,8 +312,8 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
 _TORCH_DT = {0: torch.float16, W4A16_BF16: torch.bfloat16}
 
 
-def _gemm_args(where, X, packed, M, Y, col_scale=None, bias=None, aux=None, activation="none",
-               aux_op="add"):
+def _gemm_args(where, X, packed, M, Y, stream, col_scale=None, bias=None, aux=None,
+               activation="none", aux_op="add"):
     """Checks of the tensor arguments of the GEMM entry points; returns (M, Y, ep)
     with Y allocated if not given and ep the w4a16_epilogue_t (None if no
     epilogue operand or activation is given)."""
@@ -313,7 +329,7 @@ def _gemm_args(where, X, packed, M, Y, col_scale=None, bias=None, aux=None, acti
     if packed.data.get_device() != dev_index:
         _bad(f"{where}: the blob is on {packed.data.device}, X on {X.device}")
     if Y is None:
-        Y = torch.empty((M, N), dtype=dt, device=X.device)
+        Y = _empty_on(stream, (M, N), dt, X.device)
     elif (Y.dtype != dt or Y.numel() != M * N or not Y.is_contiguous() or not Y.is_cuda
           or Y.get_device() != dev_index):
         _require(Y, f"{where}: Y", dt, M * N, X.device)
@@ -340,7 +356,7 @@ def w4a16_gemm(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
     """Y[M][N] = X[M][K] . dequant(packed); X is [M][K] fp16/bf16 on the device.
     `plan`: an optional kernel hint (see plan_flags)."""
     lib = _lib if _lib is not None else load_library()
-    M, Y, _ = _gemm_args("w4a16_gemm", X, packed, M, Y)
+    M, Y, _ = _gemm_args("w4a16_gemm", X, packed, M, Y, stream)
     K, N, G = packed.K, packed.N, packed.group_size
     flags = packed.flags if plan is None else packed.flags | plan_flags(plan)
     sh = _stream_handle(stream)
@@ -365,8 +381,8 @@ def w4a16_gemm_ex(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
     Y = aux_op(act(X.deq * col_scale + bias), aux): col_scale fp32 [N], bias [N]
     and aux [M][N] in X's dtype, each optional (device tensors)."""
     lib = load_library()
-    M, Y, ep = _gemm_args("w4a16_gemm_ex", X, packed, M, Y, col_scale, bias, aux, activation,
-                          aux_op)
+    M, Y, ep = _gemm_args("w4a16_gemm_ex", X, packed, M, Y, stream, col_scale, bias, aux,
+                          activation, aux_op)
     K, N, G = packed.K, packed.N, packed.group_size
     flags = packed.flags | plan_flags(plan)
     if workspace is None:
@@ -389,7 +405,7 @@ def w4a16_gemm_noalloc(X: torch.Tensor, packed: PackedW4, Y: torch.Tensor,
     if Y is None:
         _bad("w4a16_gemm_noalloc: Y must be provided")
     lib = load_library()
-    M, Y, ep = _gemm_args("w4a16_gemm_noalloc", X, packed, M, Y, col_scale, bias, aux,
+    M, Y, ep = _gemm_args("w4a16_gemm_noalloc", X, packed, M, Y, stream, col_scale, bias, aux,
                           activation, aux_op)
     _check(lib.w4a16_gemm_noalloc(_ptr(X), _ptr(packed.data), packed.data.numel(), _ptr(Y), M,
                                   packed.N, packed.K, packed.group_size,
@@ -403,7 +419,7 @@ def w4a16_dequant(packed: PackedW4, W_out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     K, N = packed.K, packed.N
     if W_out is None:
-        W_out = torch.empty((K, N), dtype=torch_dtype(packed.flags), device=packed.data.device)
+        W_out = _empty_on(stream, (K, N), torch_dtype(packed.flags), packed.data.device)
     _check(load_library().w4a16_dequant(_ptr(packed.data), packed.data.numel(), _ptr(W_out), K,
                                         N, packed.group_size, packed.flags, _stream(stream)),
            "w4a16_dequant")
@@ -423,7 +439,7 @@ def w4a16_read_probe(buf: torch.Tensor, nbytes: Optional[int] = None,
     if nbytes is None:
         nbytes = (buf.numel() * buf.element_size()) // 1024 * 1024
     if out is None:
-        out = torch.empty(w4a16_read_probe_out_bytes(), dtype=torch.uint8, device=buf.device)
+        out = _empty_on(stream, w4a16_read_probe_out_bytes(), torch.uint8, buf.device)
     _check(lib.w4a16_read_probe(_ptr(buf), nbytes, _ptr(out), out.numel(), _stream(stream)),
            "w4a16_read_probe")
     return out
@@ -431,7 +447,7 @@ def w4a16_read_probe(buf: torch.Tensor, nbytes: Optional[int] = None,
 
 def w4a16_mfma_layout_probe(A: torch.Tensor, B: torch.Tensor, flags: int,
                             stream=None) -> torch.Tensor:
-    D = torch.empty((32, 32), dtype=torch.float32, device=A.device)
+    D = _empty_on(stream, (32, 32), torch.float32, A.device)
     _check(load_library().w4a16_mfma_layout_probe(_ptr(A), _ptr(B), _ptr(D), flags,
                                                   _stream(stream)), "w4a16_mfma_layout_probe")
     return D

@@ -16,7 +16,8 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _ptr, _require, _stream, _stream_handle, load_library, workspace_for)
+               _bad, _check, _empty_on, _ptr, _require, _stream, _stream_handle, load_library,
+               workspace_for)
 
 FP8_LAYOUT_VERSION = 1
 FP8_BLOCK = 128
@@ -96,7 +97,7 @@ def fp8_repack(w: torch.Tensor, ws: torch.Tensor, stream=None) -> PackedFP8:
         raise W4A16Error(W4A16_ERR_UNSUPPORTED if K % 16 else W4A16_ERR_INVALID_ARG,
                          "fp8_packed_bytes")
     _require(ws, "fp8_repack: ws", torch.float32, E * _blocks(N) * _blocks(K), w.device)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+    packed = _empty_on(stream, nbytes, torch.uint8, w.device)
     _check(_lib().fp8_repack(_ptr(w), _ptr(ws), E, K, N, _ptr(packed), nbytes, _stream(stream)),
            "fp8_repack")
     return PackedFP8(packed, E, K, N, w.dim() == 3)
@@ -138,7 +139,7 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
         _bad("fp8_gemm: the blob holds experts")
     N = packed.N
     if Y is None:
-        Y = torch.empty((M, N), dtype=tdt, device=xq.device)
+        Y = _empty_on(stream, (M, N), tdt, xq.device)
     else:
         _require(Y, "fp8_gemm: Y", tdt, M * N, xq.device)
     flags = flag if plan is None else flag | plan_flags_fp8(plan)
@@ -167,7 +168,7 @@ def fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, offs
         R = rows.numel()
         _require(rows, f"{where}: rows", torch.int32, R, xq.device)
     if Y is None:
-        Y = torch.empty((R, N), dtype=tdt, device=xq.device)
+        Y = _empty_on(stream, (R, N), tdt, xq.device)
     else:
         _require(Y, f"{where}: Y", tdt, R * N, xq.device)
     flags = flag if plan is None else flag | plan_flags_fp8(plan)

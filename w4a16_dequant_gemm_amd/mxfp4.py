@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _ptr, _require, _stream, load_library)
+               _bad, _check, _empty_on, _ptr, _require, _stream, load_library)
 
 MXFP4_LAYOUT_VERSION = 1
 MXFP4_PLAN = {"stream": 0x10, "tiled": 0x20}
@@ -72,7 +72,7 @@ def mxfp4_repack(qweight: torch.Tensor, ws: torch.Tensor, K: int, N: int, stream
             or not qweight.is_contiguous() or not qweight.is_cuda:
         _bad("mxfp4_repack: qweight must be a contiguous int32 device tensor of K/8*N elements")
     _require(ws, "mxfp4_repack: ws", torch.uint8, (K // 32) * N, dev)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    packed = _empty_on(stream, nbytes, torch.uint8, dev)
     _check(_lib().mxfp4_repack(_ptr(qweight), _ptr(ws), K, N, _ptr(packed), nbytes,
                                _stream(stream)), "mxfp4_repack")
     return PackedMX(packed, K, N)
@@ -86,8 +86,8 @@ def mxfp4_quantize_rows(X: torch.Tensor, stream=None):
     M, K = X.shape
     if K % 32:
         _bad("mxfp4_quantize_rows: K must be a multiple of 32")
-    xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
-    xs = torch.empty((M, K // 32), dtype=torch.uint8, device=X.device)
+    xq = _empty_on(stream, (M, K), torch.uint8, X.device)
+    xs = _empty_on(stream, (M, K // 32), torch.uint8, X.device)
     flags = 0x1 if X.dtype == torch.bfloat16 else 0x0
     _check(_lib().mxfp4_quantize_rows(_ptr(X), _ptr(xq), _ptr(xs), M, K, flags, _stream(stream)),
            "mxfp4_quantize_rows")
@@ -107,7 +107,7 @@ def mxfp4_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedMX, out: str = 
     N = packed.N
     _require(xs, "mxfp4_gemm: xs", torch.uint8, M * (K // 32), xq.device)
     if Y is None:
-        Y = torch.empty((M, N), dtype=tdt, device=xq.device)
+        Y = _empty_on(stream, (M, N), tdt, xq.device)
     _require(Y, "mxfp4_gemm: Y", tdt, M * N, xq.device)
     if packed.data.device != xq.device:
         _bad("mxfp4_gemm: the blob is on another device")

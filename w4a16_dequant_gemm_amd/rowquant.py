@@ -17,8 +17,8 @@ from typing import Optional
 
 import torch
 
-from . import (W4A16Error, W4A16_ERR_UNSUPPORTED, _bad, _check, _require, _stream_handle,
-               load_library)
+from . import (W4A16Error, W4A16_ERR_UNSUPPORTED, _bad, _check, _empty_on, _require,
+               _stream_handle, load_library)
 
 ROWQUANT_KIND = {"fp8": 0x00, "int8": 0x10, "mx": 0x20, "x16": 0x30}
 ROWQUANT_MAX_ROW = 131072
@@ -67,7 +67,7 @@ def _same(t: torch.Tensor, like: torch.Tensor, where: str, name: str) -> int:
     return _input(t, where, name)[2]
 
 
-def _outputs(where: str, like: torch.Tensor, T: int, W: int, kind: str, q, s):
+def _outputs(where: str, like: torch.Tensor, T: int, W: int, kind: str, q, s, stream):
     """The output tensors (made if not given) and the call's flags."""
     spec = _KINDS.get(kind)
     if spec is None:
@@ -79,8 +79,8 @@ def _outputs(where: str, like: torch.Tensor, T: int, W: int, kind: str, q, s):
         q_dtype = like.dtype
     if q is None:
         # empty_like: 1.2 us where empty with a shape and a device takes 1.7
-        q = (torch.empty_like(like, dtype=q_dtype) if like.is_contiguous()
-             else torch.empty((T, W), dtype=q_dtype, device=like.device))
+        q = (torch.empty_like(like, dtype=q_dtype) if stream is None and like.is_contiguous()
+             else _empty_on(stream, (T, W), q_dtype, like.device))
     else:
         _require(q, f"{where}: q", q_dtype, T * W, like.device)
     if s_dtype is None:
@@ -89,7 +89,7 @@ def _outputs(where: str, like: torch.Tensor, T: int, W: int, kind: str, q, s):
     else:
         shape = (T, -(-W // 128)) if kind == "fp8" else (T, W // 32) if kind == "mx" else (T,)
         if s is None:
-            s = torch.empty(shape, dtype=s_dtype, device=like.device)
+            s = _empty_on(stream, shape, s_dtype, like.device)
         else:
             _require(s, f"{where}: s", s_dtype, T * (shape[1] if len(shape) == 2 else 1),
                      like.device)
@@ -111,12 +111,12 @@ def rmsnorm_quantize_rows(x: torch.Tensor, weight: torch.Tensor,
     if (weight.dtype != x.dtype or weight.numel() != W or not weight.is_contiguous()
             or weight.get_device() != x.get_device()):
         _require(weight, f"{where}: weight", x.dtype, W, x.device)   # raises with the details
-    q, s, flags = _outputs(where, x, T, W, kind, q, s)
+    q, s, flags = _outputs(where, x, T, W, kind, q, s, stream)
     if h is not None:
         _require(h, f"{where}: h", x.dtype, T * W, x.device)
     elif residual is not None:
-        h = (torch.empty_like(x) if x.is_contiguous()
-             else torch.empty((T, W), dtype=x.dtype, device=x.device))
+        h = (torch.empty_like(x) if stream is None and x.is_contiguous()
+             else _empty_on(stream, (T, W), x.dtype, x.device))
     _check(_lib().rowquant_rmsnorm(x.data_ptr(), ldx,
                                    None if residual is None else residual.data_ptr(), ldr,
                                    weight.data_ptr(), eps, None if h is None else h.data_ptr(),
@@ -133,7 +133,7 @@ def swiglu_quantize_rows(gate: torch.Tensor, up: torch.Tensor, kind: str = "fp8"
     where = "swiglu_quantize_rows"
     T, W, ldg = _input(gate, where, "gate")
     ldu = _same(up, gate, where, "up")
-    q, s, flags = _outputs(where, gate, T, W, kind, q, s)
+    q, s, flags = _outputs(where, gate, T, W, kind, q, s, stream)
     _check(_lib().rowquant_swiglu(gate.data_ptr(), ldg, up.data_ptr(), ldu, q.data_ptr(),
                                   None if s is None else s.data_ptr(), T, W, flags,
                                   _stream_handle(stream)), where)

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _ptr, _require, _stream, load_library)
+               _bad, _check, _empty_on, _ptr, _require, _stream, load_library)
 
 W4A8_LAYOUT_VERSION = 1
 W4A8_OUT = {"fp16": 0x0, "bf16": 0x1, "i32": 0x2}
@@ -85,7 +85,7 @@ def w4a8_repack(qweight: torch.Tensor, s8: torch.Tensor, a: torch.Tensor, sw: to
     _require(s8, "w4a8_repack: s8", torch.uint8, ng, dev)
     _require(a, "w4a8_repack: a", torch.uint8, ng, dev)
     _require(sw, "w4a8_repack: sw", torch.float32, N, dev)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    packed = _empty_on(stream, nbytes, torch.uint8, dev)
     _check(_lib().w4a8_repack(_ptr(qweight), _ptr(s8), _ptr(a), _ptr(sw), K, N, group_size,
                               _ptr(packed), nbytes, _stream(stream)), "w4a8_repack")
     return PackedW8(packed, K, N, group_size)
@@ -99,7 +99,7 @@ def trailer_flags(packed: PackedW8) -> int:
 
 def w4a8_dequant(packed: PackedW8, stream=None) -> torch.Tensor:
     K, N, G = packed.K, packed.N, packed.group_size
-    W = torch.empty((K, N), dtype=torch.int8, device=packed.data.device)
+    W = _empty_on(stream, (K, N), torch.int8, packed.data.device)
     _check(_lib().w4a8_dequant(_ptr(packed.data), packed.data.numel(), _ptr(W), K, N, G,
                                _stream(stream)), "w4a8_dequant")
     return W
@@ -113,9 +113,9 @@ def w4a8_quantize_rows(X: torch.Tensor, xq: Optional[torch.Tensor] = None,
         _bad("w4a8_quantize_rows: X must be a contiguous fp16/bf16 [M][K] device tensor")
     M, K = X.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        xq = _empty_on(stream, (M, K), torch.int8, X.device)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+        sx = _empty_on(stream, M, torch.float32, X.device)
     _require(xq, "w4a8_quantize_rows: xq", torch.int8, M * K, X.device)
     _require(sx, "w4a8_quantize_rows: sx", torch.float32, M, X.device)
     flags = W4A8_X["bf16" if X.dtype == torch.bfloat16 else "fp16"]
@@ -138,7 +138,7 @@ def w4a8_gemm(xq: torch.Tensor, sx: Optional[torch.Tensor], packed: PackedW8, ou
     if out != "i32" or sx is not None:
         _require(sx, "w4a8_gemm: sx", torch.float32, M, xq.device)
     if Y is None:
-        Y = torch.empty((M, N), dtype=_OUT_DTYPE[out], device=xq.device)
+        Y = _empty_on(stream, (M, N), _OUT_DTYPE[out], xq.device)
     _require(Y, "w4a8_gemm: Y", _OUT_DTYPE[out], M * N, xq.device)
     if packed.data.device != xq.device:
         _bad("w4a8_gemm: the blob is on another device")
