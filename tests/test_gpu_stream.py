@@ -88,3 +88,32 @@ def test_rows_dropped_in_a_chain_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
         del junk
+
+
+def test_graphs_that_make_their_own_workspaces():
+    """Two graphs captured on one stream with no workspace given, replayed in the other
+    order first, with calls outside between the replays."""
+    cases = [whole_numbers(100, 4096, 512, 5), whole_numbers(90, 8192, 512, 6)]
+    for M, (xq, _, _, want) in zip((100, 90), cases):
+        assert f8().fp8_workspace_bytes(M, 512, xq.shape[1]) > 0
+    side = torch.cuda.Stream()
+    graphs = []
+    for xq, xs, packed, want in cases:
+        Y = torch.empty_like(want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            f8().fp8_gemm(xq, xs, packed, Y=Y)
+            f8().fp8_gemm(xq, xs, packed, Y=Y)     # the same workspace again
+        graphs.append((graph, Y, want))
+    for rep in range(3):
+        for graph, Y, want in reversed(graphs):
+            say(f"replay {rep}")
+            Y.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(Y, want), rep
+        for xq, xs, packed, want in cases:
+            got = f8().fp8_gemm(xq, xs, packed, stream=side)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)

@@ -29,6 +29,9 @@ class Streams:
         monkeypatch.setattr(torch, "zeros", noted)
         monkeypatch.setattr(w4, "_workspaces", {})
         monkeypatch.setattr(w4, "_retired_workspaces", [])
+        monkeypatch.setattr(w4, "_captured_workspaces", {}, raising=False)
+        self.capture = None
+        monkeypatch.setattr(w4, "_capture_number", lambda handle: self.capture, raising=False)
 
     @contextlib.contextmanager
     def use(self, stream):
@@ -49,6 +52,28 @@ def test_workspace_is_filled_on_the_stream_that_uses_it(streams, handle):
     assert w4._workspace_at(1 << 20, 0, handle) is ws
     w4._workspace_at((1 << 20) + 1, 0, handle)        # grows
     assert streams.made == [("zeros", handle)] * 2
+
+
+def test_workspace_made_in_a_capture_serves_that_capture_alone(streams):
+    """Its fill runs when that graph does: another graph, or a call outside, that found it
+    would read counters no one has cleared."""
+    streams.capture = 7
+    first = w4._workspace_at(1 << 20, 0, 0x20)
+    assert w4._workspace_at(1 << 10, 0, 0x20) is first
+    streams.capture = 8
+    second = w4._workspace_at(1 << 20, 0, 0x20)
+    assert second is not first
+    streams.capture = None
+    outside = w4._workspace_at(1 << 20, 0, 0x20)
+    assert outside is not first and outside is not second
+    assert streams.made == [("zeros", 0x20)] * 3
+    # one made and filled outside serves captures too, until they need a larger one
+    streams.capture = 9
+    assert w4._workspace_at(1 << 20, 0, 0x20) is outside
+    larger = w4._workspace_at(1 << 21, 0, 0x20)
+    assert larger.numel() == 1 << 21 and w4._workspace_at(1 << 21, 0, 0x20) is larger
+    streams.capture = None
+    assert w4._workspace_at(1 << 20, 0, 0x20) is outside
 
 
 class FakeLibrary:

@@ -278,8 +278,24 @@ def w4a16_unrepack(packed: PackedW4, stream=None):
 # that has to grow is replaced, and the old one is kept alive for the rest of
 # the process: a kernel still running on its stream, or a captured graph, may
 # hold its address.
+#
+# The fill of a workspace made while its stream is captured is a node of that
+# graph and runs when the graph does: such a workspace serves the calls of that
+# capture alone, kept in _captured_workspaces as (capture's number, workspace).
 _workspaces = {}
 _retired_workspaces = []
+_captured_workspaces = {}
+
+
+def _capture_number(stream_handle: int) -> Optional[int]:
+    """The number of the capture `stream_handle` is in, or None."""
+    if stream_handle == 0:      # the default stream cannot be captured
+        return None
+    status, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    # the HIP runtime that the library is linked to
+    load_library().hipStreamGetCaptureInfo(ctypes.c_void_p(stream_handle), ctypes.byref(status),
+                                           ctypes.byref(number))
+    return number.value if status.value == 1 else None   # 1: hipStreamCaptureStatusActive
 
 
 def workspace_for(nbytes: int, device: torch.device, stream=None) -> Optional[torch.Tensor]:
@@ -297,15 +313,23 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
     ws = _workspaces.get(key)
     if ws is not None and ws.numel() >= nbytes:
         return ws
+    capture = _capture_number(stream_handle)
+    if capture is not None:
+        number, captured = _captured_workspaces.get(key, (None, None))
+        if number == capture and captured.numel() >= nbytes:
+            return captured
+    elif ws is not None:
+        _retired_workspaces.append(ws)
     size = 1 << 20
     while size < nbytes:
         size *= 2
-    if ws is not None:
-        _retired_workspaces.append(ws)
     # filled on the stream of the calls that will use it: nothing else orders the two
     with _on_stream(device_index, stream_handle):
         ws = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", device_index))
-    _workspaces[key] = ws
+    if capture is not None:
+        _captured_workspaces[key] = (capture, ws)
+    else:
+        _workspaces[key] = ws
     return ws
 
 
