@@ -249,3 +249,74 @@ def test_another_stream_and_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), rep
+
+
+# Gates beyond which exp(-gate) or the result leaves fp32's normal numbers, and factors that
+# bring the result back into them.
+FAR = {"fp16": ([-86.9, -87.5, -88.0, -90.0, -95.0, -100.0, -103.0, -104.0, -110.0, -200.0, -1e4,
+                 -65504.0, 88.0, 1e4], [1.0, 100.0, 65504.0]),
+       "bf16": ([-86.9, -87.5, -88.0, -90.0, -95.0, -100.0, -103.0, -104.0, -110.0, -150.0, -199.0,
+                 -200.0, -201.0, -1e4, -3e38, 88.0, 90.0],
+                [2.0 ** -100, 1.0, 100.0, 2.0 ** 60, 2.0 ** 100, 2.0 ** 127])}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_far_gates_keep_their_definition(kind, dtype):
+    """Whole rows of one far gate, up of one magnitude.  v is an fp32 number: where its own
+    value is subnormal it is off by up to a step, 2^-149, and what lies below half of that is 0."""
+    W = 256
+    gates, ups = FAR[dtype]
+    g = torch.tensor(gates, dtype=torch.float64).repeat_interleave(len(ups))[:, None].repeat(1, W)
+    gen = torch.Generator().manual_seed(51)
+    u = torch.tensor(ups, dtype=torch.float64).repeat(len(gates))[:, None]
+    u = u * (0.25 + 0.75 * torch.rand(len(g), W, generator=gen, dtype=torch.float64))
+    u *= torch.randint(0, 2, u.shape, generator=gen) * 2 - 1
+    g, u = g.to(DT[dtype]).cuda(), u.to(DT[dtype]).cuda()
+    v = g.double() / (1 + torch.exp(-g.double())) * u.double()
+    keep = v.abs().amax(1) < 3e38                       # results that fp32 holds
+    if kind == "x16":
+        keep &= v.abs().amax(1) < torch.finfo(DT[dtype]).max
+    g, u, v = g[keep], u[keep], v[keep]
+    assert len(g) > len(gates)
+    say(f"far gates {kind} {dtype}: {len(g)} rows")
+    q, s = rq().swiglu_quantize_rows(g, u, kind=kind)
+    torch.cuda.synchronize()
+    vrel, step = VREL["swiglu"], 2.0 ** -149
+    off = vrel * v.abs() + step                         # how far the kernel's v may be off
+    if kind == "x16":
+        info = torch.finfo(DT[dtype])
+        err = (q.double() - v).abs()
+        assert bool((err <= off + v.abs() * info.eps / 2 + info.smallest_normal * info.eps / 2).all())
+        return
+    size = {"fp8": 128, "mx": 32, "int8": W}[kind]
+    top = v.abs().view(len(v), -1, size).amax(-1)
+    top_off = off.view(len(v), -1, size).amax(-1)
+    if kind == "mx":
+        lo = torch.floor(torch.log2((top - top_off).clamp(min=2.0 ** -300))) - 8
+        hi = torch.floor(torch.log2(top + top_off)) - 8
+        e = s.double() - 127
+        assert bool(((e >= lo.clamp(min=-127)) & (e <= hi.clamp(min=-127))).all())
+        unit = torch.exp2(e)
+    else:
+        s = s.double().view(len(v), -1)
+        want = top.clamp(min=2.0 ** -110) / 448 if kind == "fp8" else top / 127
+        # the scale's own rounding, subnormal ones (int8) included
+        assert bool(((s - want).abs() <= top_off / 127 + want * 2.0 ** -22 + step).all())
+        unit = torch.where(s > 0, s, 1.0)
+    unit = unit.repeat_interleave(size, 1)
+    t = v / unit
+    # what v's error is in codes; the product with 448 / max and its factor's rounding
+    slack = off / unit + 2.0 ** -22 * t.abs()
+    if kind == "int8":
+        t = t.clamp(-127, 127)      # a subnormal scale is rounded so far that v / s passes 127
+        assert bool(((q.double() - t).abs() <= 0.5 + slack)[top.repeat_interleave(size, 1) > 0].all())
+        zero = v.abs().amax(1) < step / 2 * (1 - vrel)
+        assert bool((q[zero] == 0).all()) and bool((s[zero] == 0).all())
+        return
+    t = t.clamp(-448, 448)
+    got = q.view(torch.float8_e4m3fn).float().double()
+    assert bool(((got - t).abs() <= e4m3_half_step(t) + slack).all())
+    # nothing of a block that vanishes remains
+    gone = (top < 2.0 ** -151).repeat_interleave(size, 1)
+    assert bool(gone.any()) and bool((got[gone] == 0).all())

@@ -72,25 +72,72 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[kPiece]) {
     *((u32x4*)p + 1) = b;
 }
 
-// g / (1 + exp(-g)).  exp2's argument is split into a rounded product and its
-// remainder (the low part of log2 e included), so the exponential is good to about
-// one unit in the last place, and the quotient is the product with the reciprocal
-// corrected by its remainder: the instructions' own units (one each) would flip
-// codes next to a border.  Below -88, where the result is under 2^-119, g is taken
-// as -88; the exponent's argument stops at 128, where the exponential is 0.
-__device__ __forceinline__ float silu(float g) {
+// exp(x) = 2^n (1 + l) exp2(h) with h + n = x * log2 e rounded and l the natural
+// logarithm of what that rounding and the low part of log2 e lost: good to about
+// one unit in the last place.
+__device__ __forceinline__ float exp_scaled(float x, float n) {
+#pragma clang fp contract(off)   // h + n is the rounded h that l belongs to
     constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
     constexpr float kLowLn2 = 0x1.4ae0cp-26f * kLn2;   // the low part of log2 e, times ln 2
-    const float m = -__builtin_amdgcn_fmed3f(g, -88.0f, 128.0f);
-    g = __builtin_amdgcn_fmed3f(g, -88.0f, 0x1.fffffep+127f);
-    const float h = m * kLog2e;
-    const float l = __builtin_fmaf(__builtin_fmaf(m, kLog2e, -h), kLn2, m * kLowLn2);
-    float e = __builtin_amdgcn_exp2f(h);
-    e = __builtin_fmaf(e, l, e);
-    const float d = 1.0f + e;
+    const float h = x * kLog2e;
+    const float l = __builtin_fmaf(__builtin_fmaf(x, kLog2e, -h), kLn2, x * kLowLn2);
+    const float e = __builtin_amdgcn_exp2f(h + n);
+    return __builtin_fmaf(e, l, e);
+}
+
+constexpr float kFarGate = 87.0f;   // exp(87) and its reciprocal are normal numbers
+
+// g / (1 + exp(-g)) for |g| <= kFarGate or NaN.  The quotient is the product with the
+// reciprocal corrected by its remainder: the instructions' own units (one each)
+// would flip codes next to a border.
+__device__ __forceinline__ float silu_near(float g) {
+    const float d = 1.0f + exp_scaled(-g, 0.0f);
     const float r = __builtin_amdgcn_rcpf(d);
     const float q = g * r;
     return __builtin_fmaf(__builtin_fmaf(-d, q, g), r, q);
+}
+
+// g / (1 + exp(-g)) * u for any g.  Beyond kFarGate the sum is 1 or exp(-g) to the last
+// bit.  Below it g exp(g) leaves the normal numbers before its product with u
+// does, so 2^160 is kept apart until the end; from -200 on the product is 0 in fp32
+// whatever u (and NaN at minus infinity, as the quotient is).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    if (g > kFarGate) return g * u;
+    if (g < -kFarGate) {
+        if (g < -200.0f) g = (g - g) - 200.0f;
+        return g * exp_scaled(g, 160.0f) * (u * 0x1p-80f) * 0x1p-80f;
+    }
+    return silu_near(g) * u;
+}
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Whether some magnitude of a piece is above kFarGate, or NaN: 16-bit floats order as
+// their bits do.
+__device__ __forceinline__ bool any_far(const Raw& g) {
+    constexpr uint16_t kBits = BF16 ? 0x42AE : 0x5570;   // of kFarGate
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (i < 4 ? g.a[i] : g.b[i - 4]) & 0x7FFF7FFFu;
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w));
+    }
+    return max(top[0], top[1]) > kBits;
+}
+
+// silu(gate) * up of a piece; a far gate sends the piece the long way.
+__device__ __forceinline__ void gated16(float (&v)[kPiece], Raw g, Raw u) {
+    if (!any_far(g)) {
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) v[i] = silu_near(element(g, i)) * element(u, i);
+    } else {
+        asm volatile("" : "+v"(g.a), "+v"(g.b), "+v"(u.a), "+v"(u.b));   // nothing of it is made ahead
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) {
+            v[i] = silu_mul(element(g, i), element(u, i));
+            __builtin_amdgcn_sched_barrier(0);   // one by one: no more registers than the short way
+        }
+    }
 }
 
 // 16 values times r as E4M3 codes; v_cvt_pk_fp8_f32 rounds to nearest even.  SAT:
@@ -235,14 +282,11 @@ __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
 #pragma unroll
     for (int j = 0; j < PPT; ++j) {
         const int p = threadIdx.x + j * THREADS;
+        if constexpr (!NORM) gated16(v[j], ra[j], rb[j]);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-            if constexpr (NORM) {
-                v[j][i] = element(ra[j], i) + element(rb[j], i);
-                sum = __builtin_fmaf(v[j][i], v[j][i], sum);
-            } else {
-                v[j][i] = silu(element(ra[j], i)) * element(rb[j], i);
-            }
+        for (int i = 0; NORM && i < kPiece; ++i) {
+            v[j][i] = element(ra[j], i) + element(rb[j], i);
+            sum = __builtin_fmaf(v[j][i], v[j][i], sum);
         }
         if constexpr (NORM)
             if (a.h && p < pieces) store16((uint16_t*)a.h + row * a.W + p * kPiece, v[j]);
@@ -295,8 +339,7 @@ __global__ __launch_bounds__(kFlatThreads) void swiglu_flat_kernel(RowArgs a) {
         ru = load16((const uint16_t*)a.b + row * a.ldb + piece * kPiece);
     }
     float v[kPiece];
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = silu(element(rg, i)) * element(ru, i);
+    gated16(v, rg, ru);
     emit<KIND>(v, live, row * a.W + piece * kPiece, item, (int)(idx & 7), a.q, a.s,
                RowScale{0.0f, 0.0f});
 }
