@@ -15,7 +15,11 @@
  *                  mxfp4_quantize_rows; for mxfp4_gemm.
  *   ROWQUANT_X16   q in the inputs' dtype [T][W], s NULL; for w4a16_gemm.
  * Roundings to E4M3 are to the nearest value, ties to the even code,
- * saturating at 448.  Inputs must be finite.
+ * saturating at 448.  A v that is NaN or infinite (an input that is, or a result
+ * beyond fp32) shows: in its element (X16), as a NaN or infinite scale of its block
+ * (FP8) or row (INT8), as the scale 0xFF, the E8M0 NaN (MX); such a block's or row's
+ * codes mean nothing.  Other blocks and rows are as without it, except that one such
+ * input of the norm is in its whole row's mean.
  *
  * Conventions are those of w4a16.h.  W % 16 == 0 (MX: W % 32 == 0), otherwise
  * W4A16_ERR_UNSUPPORTED; row strides (in elements) are multiples of 8 and at

@@ -320,3 +320,87 @@ def test_far_gates_keep_their_definition(kind, dtype):
     # nothing of a block that vanishes remains
     gone = (top < 2.0 ** -151).repeat_interleave(size, 1)
     assert bool(gone.any()) and bool((got[gone] == 0).all())
+
+
+def spoil(t, bad):
+    """`bad` in row 1 at 0 and 37, row 3 at the end; returns the spoilt elements."""
+    where = torch.zeros(t.shape, dtype=torch.bool, device=t.device)
+    where[1, 0] = where[1, 37] = where[3, -1] = True
+    t[where] = bad
+    return where
+
+
+def shows(kind, q, s, where):
+    """Which blocks (rows for int8, elements for x16) hold a spoilt element, and which say so."""
+    T, W = where.shape
+    if kind == "x16":
+        return where, ~torch.isfinite(q.float())
+    size = {"fp8": 128, "mx": 32, "int8": W}[kind]
+    s = s.view(T, -1)
+    return (where.view(T, -1, size).any(-1),
+            s == 255 if kind == "mx" else ~torch.isfinite(s))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_what_is_not_finite_shows(kind, dtype, bad):
+    T, W = 5, 2304
+    say(f"not finite {kind} {dtype} {bad}")
+    g, u = rows(T, W, dtype, 61), rows(T, W, dtype, 62)
+    clean_q, clean_s = rq().swiglu_quantize_rows(g, u, kind=kind)
+    for side in ("gate", "up"):
+        g2, u2 = g.clone(), u.clone()
+        where = spoil(g2 if side == "gate" else u2, bad)
+        q, s = rq().swiglu_quantize_rows(g2, u2, kind=kind)
+        want, got = shows(kind, q, s, where)
+        assert torch.equal(got, want), side
+        size = W // want.shape[1]
+        same = ~want.repeat_interleave(size, 1)
+        assert torch.equal(q.view(torch.int16 if kind == "x16" else torch.uint8)[same],
+                           clean_q.view(torch.int16 if kind == "x16" else torch.uint8)[same])
+        if kind != "x16":
+            assert torch.equal(s.view(T, -1)[~want], clean_s.view(T, -1)[~want])
+    w = torch.ones(W, dtype=DT[dtype], device="cuda")
+    clean_q, clean_s, _ = rq().rmsnorm_quantize_rows(g, w, kind=kind)
+    g2 = g.clone()
+    where = spoil(g2, bad)
+    q, s, _ = rq().rmsnorm_quantize_rows(g2, w, kind=kind)
+    want, got = shows(kind, q, s, where)
+    assert bool(got[want].all())
+    clean = torch.tensor([0, 2, 4], device="cuda")
+    assert torch.equal(q[clean].view(torch.uint8), clean_q[clean].view(torch.uint8))
+    assert not bool(got[clean].any())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "mx"])
+@pytest.mark.parametrize("rows_", [4, 40])
+def test_what_is_not_finite_shows_in_the_product(kind, rows_):
+    from w4a16_dequant_gemm_amd import fp8, mxfp4, w4a8
+    K, N = 1024, 256
+    say(f"not finite through the product {kind} {rows_} rows")
+    gen = torch.Generator().manual_seed(63)
+    if kind == "fp8":
+        w = torch.randint(0, 127, (N, K), generator=gen, dtype=torch.uint8).cuda()
+        packed = fp8.fp8_repack(w, torch.full((2, 8), 1e-3, device="cuda"))
+        product = lambda q, s: fp8.fp8_gemm(q, s, packed)            # noqa: E731
+    else:
+        code = torch.randint(-2 ** 31, 2 ** 31 - 1, (K // 8, N), generator=gen).to(torch.int32).cuda()
+        if kind == "mx":
+            packed = mxfp4.mxfp4_repack(code, torch.full((K // 32, N), 120, dtype=torch.uint8,
+                                                         device="cuda"), K, N)
+            product = lambda q, s: mxfp4.mxfp4_gemm(q, s, packed, out="bf16")   # noqa: E731
+        else:
+            one = torch.ones(K // 128, N, dtype=torch.uint8, device="cuda")
+            packed = w4a8.w4a8_repack(code, one, one, torch.ones(N, device="cuda"), K, N, 128)
+            product = lambda q, s: w4a8.w4a8_gemm(q, s, packed, out="bf16")     # noqa: E731
+    g, u = rows(rows_, K, "bf16", 64), rows(rows_, K, "bf16", 65)
+    clean = product(*rq().swiglu_quantize_rows(g, u, kind=kind))
+    assert bool(torch.isfinite(clean.float()).all())
+    for bad in (float("nan"), float("inf")):
+        u2 = u.clone()
+        u2[2, 700] = bad
+        got = product(*rq().swiglu_quantize_rows(g, u2, kind=kind))
+        assert not bool(torch.isfinite(got[2].float()).any())
+        keep = torch.arange(rows_, device="cuda") != 2
+        assert torch.equal(got[keep], clean[keep])

@@ -157,10 +157,15 @@ __device__ __forceinline__ u32x4 codes16(const float (&v)[kPiece], float r) {
     return q;
 }
 
+// The larger one, NaN if either is: a NaN reaches its block's or row's scale.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    return __builtin_elementwise_maximum(a, b);   // v_maximum3_f32
+}
+
 __device__ __forceinline__ float amax16(const float (&v)[kPiece]) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) a = fmaxf(a, fabsf(v[i]));
+    for (int i = 0; i < kPiece; ++i) a = max_or_nan(a, fabsf(v[i]));
     return a;
 }
 
@@ -211,10 +216,10 @@ __device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_
         if (live) *(u32x4*)((uint8_t*)q + at) = w;
     } else if constexpr (KIND == KIND_FP8) {
         float a = amax16(v);
-        a = fmaxf(a, __shfl_xor(a, 1, 64));
-        a = fmaxf(a, __shfl_xor(a, 2, 64));
-        a = fmaxf(a, __shfl_xor(a, 4, 64));
-        a = fmaxf(a, kTinyMax);
+        a = max_or_nan(a, __shfl_xor(a, 1, 64));
+        a = max_or_nan(a, __shfl_xor(a, 2, 64));
+        a = max_or_nan(a, __shfl_xor(a, 4, 64));
+        a = max_or_nan(a, kTinyMax);
         const u32x4 w = codes16<false>(v, __fdiv_rn(448.0f, a));   // up to 448 and a rounding
         if (live) {
             *(u32x4*)((uint8_t*)q + at) = w;
@@ -222,13 +227,14 @@ __device__ __forceinline__ void emit(const float (&v)[kPiece], bool live, int64_
         }
     } else {
         float a = amax16(v);
-        a = fmaxf(a, __shfl_xor(a, 1, 64));
-        const int ef = (int)(__float_as_uint(a) >> 23);                 // a >= 0
+        a = max_or_nan(a, __shfl_xor(a, 1, 64));
+        const int ef = (int)((__float_as_uint(a) >> 23) & 255u);
         const int E = max(ef - 127 - 8, -127);   // floor(log2 a) - 8; subnormal a: -127 as well
         const u32x4 w = codes16<true>(v, __uint_as_float((uint32_t)(127 - E) << 23));
         if (live) {
             *(u32x4*)((uint8_t*)q + at) = w;
-            if ((piece & 1) == 0) ((uint8_t*)s)[at / 32] = (uint8_t)(E + 127);
+            // a NaN or an infinity: the E8M0 NaN
+            if ((piece & 1) == 0) ((uint8_t*)s)[at / 32] = (uint8_t)(ef == 255 ? 255 : E + 127);
         }
     }
 }
@@ -244,14 +250,14 @@ __device__ __forceinline__ float reduce_row(float x, float* part) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
         const float y = __shfl_xor(x, off, 64);
-        x = MAX ? fmaxf(x, y) : x + y;
+        x = MAX ? max_or_nan(x, y) : x + y;
     }
     if constexpr (THREADS > 64) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
         __syncthreads();
         x = part[0];
 #pragma unroll
-        for (int w = 1; w < THREADS / 64; ++w) x = MAX ? fmaxf(x, part[w]) : x + part[w];
+        for (int w = 1; w < THREADS / 64; ++w) x = MAX ? max_or_nan(x, part[w]) : x + part[w];
     }
     return x;
 }
@@ -305,7 +311,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
     if constexpr (KIND == KIND_INT8) {
         float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < PPT; ++j) m = fmaxf(m, amax16(v[j]));
+        for (int j = 0; j < PPT; ++j) m = max_or_nan(m, amax16(v[j]));
         rs = int8_scale(reduce_row<THREADS, true>(m, part[1]));
         if (threadIdx.x == 0) ((float*)a.s)[row] = rs.s;
     }
