@@ -404,3 +404,22 @@ def test_what_is_not_finite_shows_in_the_product(kind, rows_):
         assert not bool(torch.isfinite(got[2].float()).any())
         keep = torch.arange(rows_, device="cuda") != 2
         assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("W", [288, 5120, 33024, 70016])
+def test_norm_of_rows_whose_squares_leave_fp32(kind, W):
+    """bf16 rows of 2^60 and more have squares beyond fp32, rows of 2^-50 and less squares
+    that vanish beside no eps; the norm itself does not."""
+    scales = [2.0 ** 60, 2.0 ** 100, 2.0 ** 118, 2.0 ** -50, 2.0 ** -100, 2.0 ** -120, 1.0]
+    x = torch.cat([rows(1, W, "bf16", 71 + i) * c for i, c in enumerate(scales)])
+    w = (1 + 0.2 * rows(1, W, "bf16", 70).float())[0].to(torch.bfloat16)
+    for eps in (0.0, 1e-30, 1e-6):
+        say(f"norm of far rows {kind} W={W} eps={eps}")
+        for r in (None, x.flip(1) * 0.5):
+            q, s, h = rq().rmsnorm_quantize_rows(x, w, residual=r, eps=eps, kind=kind)
+            torch.cuda.synchronize()
+            check(kind, "bf16", norm_values(x, r, w, eps), q, s, VREL["norm"])
+            if r is not None:
+                want = (x.float() + r.float()).to(torch.bfloat16)
+                assert torch.equal(h.view(torch.int16), want.view(torch.int16))

@@ -264,7 +264,7 @@ __device__ __forceinline__ float reduce_row(float x, float* part) {
 
 template <int THREADS, int PPT, int KIND, bool NORM>
 __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
-    __shared__ float part[2][THREADS / 64];
+    __shared__ float part[3][THREADS / 64];   // one for each reduction of a row
     const int64_t row = blockIdx.x;
     const int pieces = (int)(a.W / kPiece);
     const uint16_t* xa = (const uint16_t*)a.a + row * a.lda;
@@ -300,8 +300,24 @@ __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
     if constexpr (NORM) {
         sum = reduce_row<THREADS, false>(sum, part[0]);
         // IEEE square root and divisions: once per row
-        const float mean = __fdiv_rn(sum, (float)a.W);
-        const float r = __fdiv_rn(1.0f, __fsqrt_rn(mean + a.eps));
+        float square = __fdiv_rn(sum, (float)a.W) + a.eps;
+        if (!(square >= 0x1p-80f && square < __builtin_inff())) {
+            // the squares left fp32 (or what they lost there counts): once more with h
+            // scaled by a power of two, which the quotient does not see.  The same
+            // for the whole workgroup.
+            const float k = square < 0x1p-80f ? 0x1p80f : 0x1p-80f;
+            sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PPT; ++j)
+#pragma unroll
+                for (int i = 0; i < kPiece; ++i) {
+                    v[j][i] *= k;
+                    sum = __builtin_fmaf(v[j][i], v[j][i], sum);
+                }
+            sum = reduce_row<THREADS, false>(sum, part[1]);
+            square = __fdiv_rn(sum, (float)a.W) + a.eps * k * k;
+        }
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(square));
 #pragma unroll
         for (int j = 0; j < PPT; ++j)
 #pragma unroll
@@ -312,7 +328,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < PPT; ++j) m = max_or_nan(m, amax16(v[j]));
-        rs = int8_scale(reduce_row<THREADS, true>(m, part[1]));
+        rs = int8_scale(reduce_row<THREADS, true>(m, part[2]));
         if (threadIdx.x == 0) ((float*)a.s)[row] = rs.s;
     }
 #pragma unroll
