@@ -1,0 +1,45 @@
+"""What the fp8 and row-quantiser bindings check of their tensors before the library is
+called, on stand-ins for device tensors (no GPU)."""
+import pytest
+import torch
+
+import w4a16_dequant_gemm_amd as w4
+from w4a16_dequant_gemm_amd import fp8, rowquant
+
+from host_fakes import FakeLibrary, FakeTensor, fake
+
+F32, U8, I32 = torch.float32, torch.uint8, torch.int32
+
+
+@pytest.fixture(autouse=True)
+def _library(monkeypatch):
+    monkeypatch.setattr(w4, "_lib", FakeLibrary())
+    monkeypatch.setattr(w4, "_stream_handle", lambda stream: 0)
+    for module in (fp8, rowquant):
+        monkeypatch.setattr(module, "_lib", FakeLibrary)
+        monkeypatch.setattr(module, "_stream_handle", lambda stream: 0)
+    monkeypatch.setattr(fp8, "_ws_bytes", {})
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None:
+                        FakeTensor(*((shape,) if isinstance(shape, int) else shape), dtype=dtype))
+    monkeypatch.setattr(torch, "empty_like", lambda like, dtype=None:
+                        FakeTensor(*like.shape, dtype=dtype or like.dtype))
+
+
+def blob(grouped=False, K=512):
+    return fp8.PackedFP8(fake(1 << 20, dtype=U8), 1, K, 128, grouped)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_scales_laid_out_by_block_are_refused(grouped):
+    """[K/128][rows] has as many numbers as [rows][K/128] and means another product."""
+    def call(xs):
+        xq = fake(6, 512, dtype=U8)
+        if grouped:
+            return fp8.fp8_grouped_gemm(xq, xs, blob(True), fake(2, dtype=I32))
+        return fp8.fp8_gemm(xq, xs, blob())
+    assert call(fake(6, 4, dtype=F32)).shape == (6, 128)
+    assert call(fake(24, dtype=F32)).shape == (6, 128)          # flat, in that order
+    assert call(fake(2, 3, 4, dtype=F32)).shape == (6, 128)
+    for shape in ((4, 6), (24, 1), (1, 24), (2, 12)):
+        with pytest.raises(w4.W4A16Error):
+            call(fake(*shape, dtype=F32))

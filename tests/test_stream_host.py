@@ -7,6 +7,8 @@ import torch
 
 import w4a16_dequant_gemm_amd as w4
 
+from host_fakes import FakeLibrary, FakeTensor, fake
+
 CURRENT = 0x10
 
 
@@ -74,46 +76,6 @@ def test_workspace_made_in_a_capture_serves_that_capture_alone(streams):
     assert larger.numel() == 1 << 21 and w4._workspace_at(1 << 21, 0, 0x20) is larger
     streams.capture = None
     assert w4._workspace_at(1 << 20, 0, 0x20) is outside
-
-
-class FakeLibrary:
-    """Takes every call and launches nothing."""
-    def __getattr__(self, name):
-        return lambda *args: (1 << 20) if name.endswith("_packed_bytes") else 0
-
-
-class FakeTensor:
-    """What the binding asks of a contiguous tensor on device 0."""
-    is_cuda = True
-    device = torch.device("cuda", 0)
-
-    def __init__(self, *shape, dtype, recorded=None):
-        self.shape, self.dtype, self.recorded = torch.Size(shape), dtype, recorded
-
-    def dim(self):
-        return len(self.shape)
-
-    def numel(self):
-        return self.shape.numel()
-
-    def stride(self, i):
-        return self.shape[i + 1:].numel()
-
-    def is_contiguous(self):
-        return True
-
-    def get_device(self):
-        return 0
-
-    def data_ptr(self):
-        return 0x10000
-
-    def record_stream(self, stream):
-        self.recorded.append(stream)
-
-
-def fake(*shape, dtype):
-    return FakeTensor(*shape, dtype=dtype)
 
 
 def calls():

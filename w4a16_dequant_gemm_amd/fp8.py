@@ -112,9 +112,13 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
     if out not in _DT:
         raise ValueError(f"bad output dtype {out!r}")
     dev = xq.get_device()
-    if (xs.dtype != torch.float32 or xs.numel() != rows * _blocks(K) or not xs.is_contiguous()
+    kb = _blocks(K)
+    if (xs.dtype != torch.float32 or xs.numel() != rows * kb or not xs.is_contiguous()
             or xs.get_device() != dev):
-        _require(xs, f"{where}: xs", torch.float32, rows * _blocks(K), xq.device)   # raises
+        _require(xs, f"{where}: xs", torch.float32, rows * kb, xq.device)   # raises
+    # the same numbers the other way round, a row of scales per block, give another product
+    if xs.dim() != 1 and xs.shape[-1] != kb:
+        _bad(f"{where}: xs is {tuple(xs.shape)}, its rows must hold {kb} scales")
     if packed.data.get_device() != dev:
         _bad(f"{where}: the blob is on another device")
     return rows, K, *_DT[out]
