@@ -43,3 +43,17 @@ def test_scales_laid_out_by_block_are_refused(grouped):
     for shape in ((4, 6), (24, 1), (1, 24), (2, 12)):
         with pytest.raises(w4.W4A16Error):
             call(fake(*shape, dtype=F32))
+
+
+@pytest.mark.parametrize("kind,dtype,n", [("fp8", F32, 5), ("mx", U8, 20)])
+def test_scale_outputs_laid_out_by_block_are_refused(kind, dtype, n):
+    x, w = fake(6, 640, dtype=torch.float16), fake(640, dtype=torch.float16)
+    calls = (lambda s: rowquant.rmsnorm_quantize_rows(x, w, kind=kind, s=s),
+             lambda s: rowquant.swiglu_quantize_rows(x, x, kind=kind, s=s))
+    for call in calls:
+        for shape in ((6, n), (6 * n,), (2, 3, n)):
+            given = fake(*shape, dtype=dtype)
+            assert call(given)[1] is given
+        for shape in ((n, 6), (6 * n, 1)):
+            with pytest.raises(w4.W4A16Error):
+                call(fake(*shape, dtype=dtype))
