@@ -57,3 +57,33 @@ def test_scale_outputs_laid_out_by_block_are_refused(kind, dtype, n):
         for shape in ((n, 6), (6 * n, 1)):
             with pytest.raises(w4.W4A16Error):
                 call(fake(*shape, dtype=dtype))
+
+
+class Elsewhere(FakeTensor):
+    """A tensor in host memory, or on another device, or with gaps."""
+
+    def __init__(self, cuda=True, index=0, contiguous=True):
+        super().__init__(1 << 20, dtype=U8)
+        self.is_cuda, self.index, self.contiguous = cuda, index, contiguous
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+
+def test_a_workspace_the_kernel_cannot_use_is_refused():
+    """Its address and element count go to the library as they are."""
+    half = torch.float16
+    p16 = w4.PackedW4(fake(1 << 20, dtype=U8), 512, 128, 128, 0, w4._layout_version)
+    calls = (lambda ws: fp8.fp8_gemm(fake(6, 512, dtype=U8), fake(6, 4, dtype=F32), blob(),
+                                     workspace=ws),
+             lambda ws: w4.w4a16_gemm(fake(6, 512, dtype=half), p16, workspace=ws),
+             lambda ws: w4.w4a16_gemm_ex(fake(6, 512, dtype=half), p16, workspace=ws))
+    for call in calls:
+        assert call(Elsewhere()).shape == (6, 128)
+        for bad in (Elsewhere(cuda=False, index=-1), Elsewhere(index=1),
+                    Elsewhere(contiguous=False)):
+            with pytest.raises(w4.W4A16Error):
+                call(bad)

@@ -308,6 +308,13 @@ def workspace_for(nbytes: int, device: torch.device, stream=None) -> Optional[to
     return _workspace_at(nbytes, index, _stream_handle(stream))
 
 
+def _require_workspace(workspace: torch.Tensor, where: str, device_index: int):
+    """A workspace from the caller: the C entry points see its address and size only."""
+    if (not workspace.is_cuda or workspace.get_device() != device_index
+            or not workspace.is_contiguous()):
+        _bad(f"{where}: the workspace must be a contiguous tensor on device {device_index}")
+
+
 def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.Tensor:
     key = (device_index, stream_handle)
     ws = _workspaces.get(key)
@@ -388,6 +395,8 @@ def w4a16_gemm(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
         need = _workspace_need(M, N, K, G, flags)
         if need:
             workspace = _workspace_at(need, X.get_device(), sh)
+    else:
+        _require_workspace(workspace, "w4a16_gemm", X.get_device())
     st = lib.w4a16_gemm(X.data_ptr(), packed.data.data_ptr(), packed.data.numel(), Y.data_ptr(),
                         M, N, K, G, flags, None if workspace is None else workspace.data_ptr(),
                         0 if workspace is None else workspace.numel(), sh)
@@ -411,6 +420,8 @@ def w4a16_gemm_ex(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
     flags = packed.flags | plan_flags(plan)
     if workspace is None:
         workspace = workspace_for(_workspace_need(M, N, K, G, flags), X.device, stream)
+    else:
+        _require_workspace(workspace, "w4a16_gemm_ex", X.get_device())
     _check(lib.w4a16_gemm_ex(_ptr(X), _ptr(packed.data), packed.data.numel(), _ptr(Y), M, N, K,
                              G, flags, None if ep is None else ctypes.byref(ep), _ptr(workspace),
                              0 if workspace is None else workspace.numel(), _stream(stream)),

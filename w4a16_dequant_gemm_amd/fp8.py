@@ -16,8 +16,8 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _empty_on, _ptr, _require, _stream, _stream_handle, load_library,
-               workspace_for)
+               _bad, _check, _empty_on, _ptr, _require, _require_workspace, _stream,
+               _stream_handle, load_library, workspace_for)
 
 FP8_LAYOUT_VERSION = 1
 FP8_BLOCK = 128
@@ -149,6 +149,8 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
     flags = flag if plan is None else flag | plan_flags_fp8(plan)
     if workspace is None:
         workspace = workspace_for(_workspace_need(M, N, K, flags), xq.device, stream)
+    else:
+        _require_workspace(workspace, "fp8_gemm", xq.get_device())
     _check(_lib().fp8_gemm(xq.data_ptr(), xs.data_ptr(), packed.data.data_ptr(),
                            packed.data.numel(), Y.data_ptr(), M, N, K, flags,
                            None if workspace is None else workspace.data_ptr(),
