@@ -1,5 +1,8 @@
 """What the fp8 and row-quantiser bindings check of their tensors before the library is
 called, on stand-ins for device tensors (no GPU)."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -8,6 +11,7 @@ from w4a16_dequant_gemm_amd import fp8, rowquant
 
 from host_fakes import FakeLibrary, FakeTensor, fake
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 F32, U8, I32 = torch.float32, torch.uint8, torch.int32
 
 
@@ -87,3 +91,17 @@ def test_a_workspace_the_kernel_cannot_use_is_refused():
                     Elsewhere(contiguous=False)):
             with pytest.raises(w4.W4A16Error):
                 call(bad)
+
+
+def test_a_blob_of_another_layout_is_refused():
+    """One kept from a library that ordered the weights otherwise."""
+    header = open(os.path.join(ROOT, "include", "fp8.h")).read()
+    assert int(re.search(r"#define FP8_LAYOUT_VERSION (\d+)", header)[1]) == fp8.FP8_LAYOUT_VERSION
+    xq, xs = fake(6, 512, dtype=U8), fake(6, 4, dtype=F32)
+    for grouped, call in ((False, lambda p: fp8.fp8_gemm(xq, xs, p)),
+                          (True, lambda p: fp8.fp8_grouped_gemm(xq, xs, p, fake(2, dtype=I32)))):
+        packed = blob(grouped)
+        assert call(packed).shape == (6, 128)
+        packed.layout_version = fp8.FP8_LAYOUT_VERSION + 1
+        with pytest.raises(w4.W4A16Error):
+            call(packed)

@@ -19,7 +19,7 @@ from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_P
                _bad, _check, _empty_on, _ptr, _require, _require_workspace, _stream,
                _stream_handle, load_library, workspace_for)
 
-FP8_LAYOUT_VERSION = 1
+FP8_LAYOUT_VERSION = 1   # of include/fp8.h
 FP8_BLOCK = 128
 FP8_PLAN = {"stream": 0x10, "tiled": 0x20}
 C_FUNCTIONS_FP8 = ("fp8_packed_bytes", "fp8_repack", "fp8_workspace_bytes", "fp8_gemm",
@@ -73,6 +73,7 @@ class PackedFP8:
     K: int
     N: int
     grouped: bool        # made from [E][N][K] (a stack of experts) or [N][K]
+    layout_version: int = FP8_LAYOUT_VERSION   # of the library that made it
 
 
 def fp8_packed_bytes(E: int, K: int, N: int) -> int:
@@ -106,6 +107,8 @@ def fp8_repack(w: torch.Tensor, ws: torch.Tensor, stream=None) -> PackedFP8:
 def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str):
     if xq.dim() != 2 or xq.dtype not in _CODES or not xq.is_cuda or not xq.is_contiguous():
         _bad(f"{where}: xq must be a contiguous E4M3 [rows][K] device tensor")
+    if packed.layout_version != FP8_LAYOUT_VERSION:
+        _bad(f"{where}: blob layout version {packed.layout_version}, library {FP8_LAYOUT_VERSION}")
     rows, K = xq.shape
     if K != packed.K:
         _bad(f"{where}: xq has K = {K}, the blob {packed.K}")
