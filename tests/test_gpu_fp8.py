@@ -324,3 +324,20 @@ def test_norm_product_activation_product():
     out = f8().fp8_gemm(q2, sc2, f8().fp8_repack(w2, s2))
     y, B = product(values(q2, sc2, True), values(w2, s2, False))
     assert_close(out, y, B, F, "down")
+
+
+def test_every_byte_of_a_blob_is_written():
+    """Equal weights give equal blobs, whatever the memory held."""
+    for E, K, N in ((None, 640, 130), (3, 144, 100), (None, 16, 1)):
+        _, _, w, ws = make(1, K, N, E=E, seed=31)
+        size = f8().fp8_packed_bytes(E or 1, K, N)
+        say(f"blob bytes E={E} K={K} N={N}")
+        blobs = []
+        for fill in (0x00, 0xA5):
+            data = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+            status = f8()._lib().fp8_repack(w.data_ptr(), ws.data_ptr(), E or 1, K, N,
+                                            data.data_ptr(), size, None)
+            torch.cuda.synchronize()
+            assert status == 0
+            blobs.append(data)
+        assert torch.equal(*blobs)

@@ -37,10 +37,12 @@ __global__ __launch_bounds__(kThreads) void repack_codes(const uint8_t* __restri
 
 __global__ __launch_bounds__(kThreads) void repack_scales(const float* __restrict__ ws,
                                                           float* __restrict__ out, int64_t n,
+                                                          int64_t room,
                                                           uint32_t* __restrict__ trailer) {
-    for (int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x; idx < n;
+    // room: up to the trailer, so that equal weights give equal blobs
+    for (int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x; idx < room;
          idx += (int64_t)gridDim.x * kThreads)
-        out[idx] = ws[idx];
+        out[idx] = idx < n ? ws[idx] : 0.0f;
     if (blockIdx.x == 0 && threadIdx.x < kTrailerBytes / 4) {
         const uint32_t words[4] = {kTrailerMagic, FP8_LAYOUT_VERSION, kBlock, 0u};
         trailer[threadIdx.x] = threadIdx.x >= 8 && threadIdx.x < 12 ? words[threadIdx.x - 8] : 0u;
@@ -61,8 +63,9 @@ hipError_t launch_repack(const uint8_t* w, const float* ws, const Layout& L, voi
     repack_codes<<<blocks_for(pieces), kThreads, 0, stream>>>(w, base, L.N, L.K, L.NB, L.KB,
                                                               pieces);
     const int64_t n = L.E * L.NB * L.KB;
-    repack_scales<<<blocks_for(n), kThreads, 0, stream>>>(ws, (float*)(base + L.s_off), n,
-                                                          (uint32_t*)(base + L.z_off));
+    const int64_t room = (int64_t)(L.z_off - L.s_off) / 4;
+    repack_scales<<<blocks_for(room), kThreads, 0, stream>>>(ws, (float*)(base + L.s_off), n, room,
+                                                             (uint32_t*)(base + L.z_off));
     return hipGetLastError();
 }
 
