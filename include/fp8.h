@@ -19,7 +19,9 @@
  *
  * Conventions are those of w4a16.h (plain C types, caller-owned 16-byte
  * aligned device pointers, stream as void*, asynchronous, nothing allocated,
- * every argument validated on the host before any HIP call).  Shapes: N >= 1,
+ * every argument validated on the host before any HIP call); scales (xs, ws)
+ * need the alignment of a float only, so that rows of them can be taken from
+ * any place in a tensor.  Shapes: N >= 1,
  * K >= 16 and K % 16 == 0 (else W4A16_ERR_UNSUPPORTED), N, K < 2^24, rows
  * <= 2^30, the codes of X below 2^36 bytes, experts <= 65535.  Zero rows are a call without work.
  */

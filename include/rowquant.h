@@ -21,7 +21,8 @@
  * codes mean nothing.  Other blocks and rows are as without it, except that one such
  * input of the norm is in its whole row's mean.
  *
- * Conventions are those of w4a16.h.  W % 16 == 0 (MX: W % 32 == 0), otherwise
+ * Conventions are those of w4a16.h, but s needs the alignment of its elements
+ * only.  W % 16 == 0 (MX: W % 32 == 0), otherwise
  * W4A16_ERR_UNSUPPORTED; row strides (in elements) are multiples of 8 and at
  * least W; T < 2^31.  T = 0 is a call without work.
  */

@@ -164,3 +164,19 @@ def test_workspace_follows_the_plan(lib, K):
     assert fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8("stream")) == 0
     small = fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8(("tiled", 3)))
     assert small == 0 or (small - 65536) % (2 * 8 * 64 * 64 * 4) == 0
+
+
+def test_scales_need_the_alignment_of_a_float(lib):
+    """What follows the checks of the pointers is the check of the workspace, so nothing is
+    launched."""
+    at = lambda n: ctypes.c_void_p(0x10000 + n)                        # noqa: E731
+    call = lambda xs: lib.fp8_gemm(FAKE, xs, FAKE, 1 << 40, FAKE, 100, 512, 4096, 0,  # noqa: E731
+                                   None, 0, None)
+    assert lib.fp8_workspace_bytes(100, 512, 4096, 0) > 0
+    for n in (0, 4, 8, 12, 100):
+        assert call(at(n)) == w4.W4A16_ERR_WORKSPACE
+    for n in (1, 2, 3, 6):
+        assert call(at(n)) == INV
+        assert lib.fp8_repack(FAKE, at(n), 1, 256, 128, FAKE, 1 << 30, None) == INV
+        assert lib.rowquant_swiglu(FAKE, 256, FAKE, 256, FAKE, at(n), 4, 256, 0, None) == INV
+        assert lib.rowquant_swiglu(FAKE, 256, FAKE, 256, FAKE, at(n), 4, 256, 0x10, None) == INV

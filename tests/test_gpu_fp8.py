@@ -341,3 +341,21 @@ def test_every_byte_of_a_blob_is_written():
             assert status == 0
             blobs.append(data)
         assert torch.equal(*blobs)
+
+
+def test_scales_from_any_place_in_a_tensor():
+    """Rows and experts cut out of larger tensors: their scales start at any float."""
+    K, N, E = 640, 130, 3                                # 5 scales a row, 10 an expert
+    xq, xs, w, ws = make(70, K, N, E=E, seed=21)
+    one = f8().fp8_repack(w[1].contiguous(), ws[1].clone())
+    cut = f8().fp8_repack(w[1].contiguous(), ws[1])
+    assert ws[1].data_ptr() % 16 and torch.equal(one.data, cut.data)
+    experts = f8().fp8_repack(w, ws)
+    off = offsets_of([20, 0, 47])
+    for plan in PLANS:
+        say(f"scales from any place plan={plan}")
+        assert xs[3:].data_ptr() % 16
+        want = f8().fp8_gemm(xq[3:].clone(), xs[3:].clone(), one, plan=plan)
+        assert torch.equal(f8().fp8_gemm(xq[3:], xs[3:], one, plan=plan), want)
+        want = f8().fp8_grouped_gemm(xq[3:].clone(), xs[3:].clone(), experts, off, plan=plan)
+        assert torch.equal(f8().fp8_grouped_gemm(xq[3:], xs[3:], experts, off, plan=plan), want)

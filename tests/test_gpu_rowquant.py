@@ -423,3 +423,19 @@ def test_norm_of_rows_whose_squares_leave_fp32(kind, W):
             if r is not None:
                 want = (x.float() + r.float()).to(torch.bfloat16)
                 assert torch.equal(h.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "mx"])
+def test_scales_go_to_any_place_in_a_tensor(kind):
+    x, u = rows(3, 640, "bf16", 81), rows(3, 640, "bf16", 82)
+    w = torch.ones(640, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda s: rq().rmsnorm_quantize_rows(x, w, kind=kind, s=s),
+                 lambda s: rq().swiglu_quantize_rows(x, u, kind=kind, s=s)):
+        want = call(None)
+        for shift in (1, 2, 3):
+            room = torch.empty(want[1].numel() + 8, dtype=want[1].dtype, device="cuda")
+            s = room[shift:shift + want[1].numel()].view(want[1].shape)
+            say(f"scales at {s.data_ptr() % 16} of 16, {kind}")
+            got = call(s)
+            assert torch.equal(s, want[1]) and torch.equal(got[0].view(torch.uint8),
+                                                           want[0].view(torch.uint8))

@@ -21,6 +21,7 @@ constexpr int64_t kMaxExperts = 65535;
 constexpr uint32_t kPlanBits = FP8_PLAN_MASK | (0xFFu << W4A16_PLAN_PARAM_SHIFT);
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }   // scales are read as floats
 
 w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
 
@@ -224,7 +225,7 @@ w4a16_status_t fp8_repack(const uint8_t* w, const float* ws, int64_t E, int64_t 
                           void* packed, size_t packed_bytes, void* stream) {
     const w4a16_status_t st = check_weights(E, K, N);
     if (st != W4A16_OK) return st;
-    if (!w || !ws || !packed || !aligned16(w) || !aligned16(ws) || !aligned16(packed))
+    if (!w || !ws || !packed || !aligned16(w) || !aligned4(ws) || !aligned16(packed))
         return W4A16_ERR_INVALID_ARG;
     const Layout L = make_layout(E, K, N);
     if (packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
@@ -249,7 +250,7 @@ w4a16_status_t fp8_gemm(const uint8_t* xq, const float* xs, const void* packed,
     if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
     if (!x_fits(M, K)) return W4A16_ERR_INVALID_ARG;
     if (M == 0) return W4A16_OK;
-    if (!xq || !xs || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(Y))
+    if (!xq || !xs || !Y || !aligned16(xq) || !aligned4(xs) || !aligned16(Y))
         return W4A16_ERR_INVALID_ARG;
     const Plan p = make_plan(M, N, K, 0, flags, num_cus());
     if (p.workspace > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.workspace))
@@ -272,7 +273,7 @@ w4a16_status_t fp8_grouped_gemm(const uint8_t* xq, const float* xs, const void* 
     if (!packed || !aligned16(packed) || packed_bytes < L.total) return W4A16_ERR_INVALID_ARG;
     if (!x_fits(T, K)) return W4A16_ERR_INVALID_ARG;
     if (R == 0) return W4A16_OK;
-    if (!xq || !xs || !offsets || !Y || !aligned16(xq) || !aligned16(xs) || !aligned16(offsets) ||
+    if (!xq || !xs || !offsets || !Y || !aligned16(xq) || !aligned4(xs) || !aligned16(offsets) ||
         !aligned16(rows) || !aligned16(Y))
         return W4A16_ERR_INVALID_ARG;
     const Plan p = make_plan(R, N, K, E, flags, num_cus());

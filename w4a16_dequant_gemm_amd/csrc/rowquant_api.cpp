@@ -33,7 +33,8 @@ bool stride_ok(int64_t ld, int64_t W) { return ld >= W && ld < kMaxDim && ld % 8
 
 bool out_ok(const void* q, const void* s, int kind) {
     if (!q || !aligned16(q)) return false;
-    return kind == KIND_X16 ? s == nullptr : s && aligned16(s);
+    if (kind == KIND_X16) return s == nullptr;
+    return s && (kind == KIND_MX || ((uintptr_t)s & 3u) == 0);   // written one by one
 }
 
 }  // namespace
