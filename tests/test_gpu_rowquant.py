@@ -439,3 +439,44 @@ def test_scales_go_to_any_place_in_a_tensor(kind):
             got = call(s)
             assert torch.equal(s, want[1]) and torch.equal(got[0].view(torch.uint8),
                                                            want[0].view(torch.uint8))
+
+
+def far_rows(T, W, dtype):
+    """Rows that differ from their neighbours, made in place (their number is large)."""
+    x = torch.empty(T, W, dtype=DT[dtype], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(91)
+    for at in range(0, T, 1 << 26):
+        x[at:at + (1 << 26)].normal_(generator=g)
+    return x
+
+
+@pytest.mark.parametrize("kind,dtype", [("int8", "bf16"), ("fp8", "fp16"), ("x16", "bf16")])
+def test_norm_of_more_rows_than_one_launch_holds(kind, dtype):
+    """64 threads a row: 2^26 rows are 2^32 work-items."""
+    T, W, most = (1 << 26) + 5, 16, ((1 << 32) - 1) // 64
+    say(f"norm of {T} rows {kind}")
+    x, w = far_rows(T, W, dtype), torch.ones(W, dtype=DT[dtype], device="cuda")
+    q, s, h = rq().rmsnorm_quantize_rows(x, w, residual=x, kind=kind)
+    for at in (slice(0, 100), slice(most - 100, most + 6), slice(T - 100, T)):
+        part = x[at].clone()
+        want = rq().rmsnorm_quantize_rows(part, w, residual=part, kind=kind)
+        for got, ref in zip((q, s, h), want):
+            if ref is not None:
+                assert torch.equal(got[at].view(torch.uint8), ref.view(torch.uint8)), at
+
+
+@pytest.mark.parametrize("kind", ["fp8", "x16"])
+def test_swiglu_of_more_rows_than_one_launch_holds(kind):
+    """8 threads a block of 128: 2^29 rows are 2^32 work-items, and 2^34 bytes."""
+    T, W, most = (1 << 29) + 3, 16, ((1 << 32) - 257) // 8
+    say(f"swiglu of {T} rows {kind}")
+    x = far_rows(T, W, "bf16")
+    q, s = rq().swiglu_quantize_rows(x, x, kind=kind)
+    for at in (slice(0, 100), slice(most - 100, most + 6), slice(T - 100, T)):
+        part = x[at].clone()
+        want = rq().swiglu_quantize_rows(part, part, kind=kind)
+        for got, ref in zip((q, s), want):
+            if ref is not None:
+                assert torch.equal(got[at].view(torch.uint8), ref.view(torch.uint8)), at
+    del x, q, s
+    torch.cuda.empty_cache()

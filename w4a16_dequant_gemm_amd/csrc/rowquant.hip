@@ -366,36 +366,54 @@ __global__ __launch_bounds__(kFlatThreads) void swiglu_flat_kernel(RowArgs a) {
                RowScale{0.0f, 0.0f});
 }
 
+// HIP counts the work-items of a launch with 32 bits: more rows take several launches.
+constexpr int64_t kMostItems = ((int64_t)1 << 32) - 1;
+
+// The call's rows first .. first + n - 1.
+template <int KIND>
+RowArgs rows_from(RowArgs a, int64_t first, int64_t n) {
+    a.a = (const uint16_t*)a.a + first * a.lda;
+    if (a.b) a.b = (const uint16_t*)a.b + first * a.ldb;
+    if (a.h) a.h = (uint16_t*)a.h + first * a.W;
+    a.q = (uint8_t*)a.q + first * a.W * (KIND == KIND_X16 ? 2 : 1);
+    if (a.s)
+        a.s = (uint8_t*)a.s + first * (KIND == KIND_FP8 ? 4 * a.KB : KIND == KIND_MX ? a.W / 32 : 4);
+    a.T = n;
+    return a;
+}
+
+template <int THREADS, int PPT, int KIND, bool NORM>
+hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
+    constexpr int64_t most = kMostItems / THREADS;
+    for (int64_t at = 0; at < a.T; at += most) {
+        const RowArgs part = rows_from<KIND>(a, at, a.T - at < most ? a.T - at : most);
+        row_kernel<THREADS, PPT, KIND, NORM><<<(unsigned)part.T, THREADS, 0, stream>>>(part);
+    }
+    return hipGetLastError();
+}
+
 template <int KIND, bool NORM>
 hipError_t launch_row(const RowArgs& a, hipStream_t stream) {
     const int64_t pieces = a.W / kPiece;
-    const unsigned grid = (unsigned)a.T;
     // the fewest threads that hold a row with one piece each, then more pieces
-    if (pieces <= 64)
-        row_kernel<64, 1, KIND, NORM><<<grid, 64, 0, stream>>>(a);
-    else if (pieces <= 256)
-        row_kernel<256, 1, KIND, NORM><<<grid, 256, 0, stream>>>(a);
-    else if (pieces <= 512)
-        row_kernel<512, 1, KIND, NORM><<<grid, 512, 0, stream>>>(a);
-    else if (pieces <= 1024)
-        row_kernel<1024, 1, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
-    else if (pieces <= 2048)
-        row_kernel<1024, 2, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
-    else if (pieces <= 4096)
-        row_kernel<1024, 4, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
-    else if (pieces <= 8192)
-        row_kernel<1024, 8, KIND, NORM><<<grid, 1024, 0, stream>>>(a);
-    else
-        return hipErrorInvalidValue;   // the entry points refuse longer rows
-    return hipGetLastError();
+    if (pieces <= 64) return launch_rows<64, 1, KIND, NORM>(a, stream);
+    if (pieces <= 256) return launch_rows<256, 1, KIND, NORM>(a, stream);
+    if (pieces <= 512) return launch_rows<512, 1, KIND, NORM>(a, stream);
+    if (pieces <= 1024) return launch_rows<1024, 1, KIND, NORM>(a, stream);
+    if (pieces <= 2048) return launch_rows<1024, 2, KIND, NORM>(a, stream);
+    if (pieces <= 4096) return launch_rows<1024, 4, KIND, NORM>(a, stream);
+    if (pieces <= 8192) return launch_rows<1024, 8, KIND, NORM>(a, stream);
+    return hipErrorInvalidValue;   // the entry points refuse longer rows
 }
 
 template <int KIND>
 hipError_t launch_flat(const RowArgs& a, hipStream_t stream) {
-    const int64_t threads = a.T * a.KB * 8;
-    const int64_t blocks = (threads + kFlatThreads - 1) / kFlatThreads;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    swiglu_flat_kernel<KIND><<<(unsigned)blocks, kFlatThreads, 0, stream>>>(a);
+    const int64_t most = (kMostItems - kFlatThreads) / (a.KB * 8);
+    for (int64_t at = 0; at < a.T; at += most) {
+        const RowArgs part = rows_from<KIND>(a, at, a.T - at < most ? a.T - at : most);
+        const int64_t blocks = (part.T * a.KB * 8 + kFlatThreads - 1) / kFlatThreads;
+        swiglu_flat_kernel<KIND><<<(unsigned)blocks, kFlatThreads, 0, stream>>>(part);
+    }
     return hipGetLastError();
 }
 
