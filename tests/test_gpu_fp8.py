@@ -359,3 +359,72 @@ def test_scales_from_any_place_in_a_tensor():
         assert torch.equal(f8().fp8_gemm(xq[3:], xs[3:], one, plan=plan), want)
         want = f8().fp8_grouped_gemm(xq[3:].clone(), xs[3:].clone(), experts, off, plan=plan)
         assert torch.equal(f8().fp8_grouped_gemm(xq[3:], xs[3:], experts, off, plan=plan), want)
+
+
+def plus_minus_one(*shape, seed):
+    """Codes of 1 and -1, made in place (their number is large)."""
+    x = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    flat = x.view(-1)
+    for at in range(0, flat.numel(), 1 << 30):
+        flat[at:at + (1 << 30)].random_(0, 2, generator=g).mul_(128).add_(0x38)
+    return x.view(E4M3)
+
+
+def test_more_tiles_than_one_launch_holds():
+    """2^30 rows, the most there can be: 2^24 tiles of 64 rows and 256 threads are 2^32
+    work-items, the rows 2^34 bytes."""
+    M, K, N = 1 << 30, 16, 8
+    xq, w = plus_minus_one(M, K, seed=41), plus_minus_one(2, N, K, seed=42)
+    xs = torch.full((M, 1), 0.5, device="cuda")
+    ws = torch.full((2, 1, 1), 0.5, device="cuda")
+    blobs = [f8().fp8_repack(w[e], ws[e]) for e in range(2)]
+    experts = f8().fp8_repack(w, ws)
+    say(f"product of {M} rows")
+    Y = f8().fp8_gemm(xq, xs, blobs[0])
+    half = M // 2 + 17
+    off = torch.tensor([0, half, M], dtype=torch.int32, device="cuda")
+    places = [slice(at, at + 300) for at in (0, M // 8 - 150, half - 150, M - M // 8 - 150, M - 300)]
+    for at in places:
+        want = (xq[at].float().double() @ w[0].float().double().t().contiguous()) / 4
+        assert torch.equal(Y[at].double(), want)
+    say(f"grouped product of {M} rows")
+    Y.fill_(float("nan"))
+    f8().fp8_grouped_gemm(xq, xs, experts, off, Y=Y)
+    for at in places:
+        y = [xq[at].float().double() @ w[e].float().double().t().contiguous() / 4 for e in (0, 1)]
+        own = torch.arange(at.start, at.stop, device="cuda")[:, None] >= half
+        assert torch.equal(Y[at].double(), torch.where(own, y[1], y[0]))
+    assert not bool(torch.isnan(Y.view(-1)[:1 << 31]).any())
+    assert not bool(torch.isnan(Y.view(-1)[1 << 31:]).any())
+    del xq, xs, Y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("plan", [("stream", 1), ("tiled", 3), None])
+def test_the_most_experts(plan):
+    """65535 experts of a row each but for some without: the streaming kernel's 136 strips
+    each are more than one launch holds, and the blob has 2^34 bytes."""
+    E, K, N = 65535, 16, 2176
+    xq, w = plus_minus_one(E, K, seed=43), plus_minus_one(E, N, K, seed=44)
+    xs = torch.full((E, 1), 0.5, device="cuda")
+    ws = torch.full((E, 17, 1), 0.5, device="cuda")
+    packed = f8().fp8_repack(w, ws)
+    counts = torch.ones(E, dtype=torch.int64, device="cuda")
+    counts[5::1000] = 0
+    counts[7::1000] += 1
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = counts.cumsum(0)
+    R = int(off[-1])
+    rows = torch.randint(0, E, (R,), generator=torch.Generator().manual_seed(45)).to(torch.int32).cuda()
+    say(f"{E} experts plan={plan}")
+    Y = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    f8().fp8_grouped_gemm(xq, xs, packed, off, rows=rows, Y=Y, plan=plan)
+    torch.cuda.synchronize()
+    expert = torch.repeat_interleave(torch.arange(E, device="cuda"), counts, output_size=R)
+    for at in range(0, R, 8192):
+        x = xq[rows[at:at + 8192].long()].float()
+        want = (x[:, None, :] * w[expert[at:at + 8192]].float()).sum(-1) / 4
+        assert torch.equal(Y[at:at + 8192].float(), want)
+    del packed, w, Y
+    torch.cuda.empty_cache()

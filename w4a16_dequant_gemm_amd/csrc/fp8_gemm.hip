@@ -136,11 +136,12 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int strips = a.NB * (kPanelTiles / NT);
-    int e = 0, strip = blockIdx.x;
+    const uint32_t block = a.first + blockIdx.x;
+    int e = 0, strip = block;
     int64_t lo = 0, hi = a.M;
     if constexpr (GROUPED) {
-        e = blockIdx.x / strips;
-        strip = blockIdx.x - e * strips;
+        e = block / strips;
+        strip = block - e * strips;
         lo = offset_at(a, e);
         hi = offset_at(a, e + 1);
     }
@@ -243,16 +244,30 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
     }
 }
 
+// A call's workgroups, `threads` each, in launches of less than 2^32 work-items (HIP
+// counts them with 32 bits).
+template <typename Launch>
+hipError_t launch_all(const GemmArgs& a, int64_t grid, int threads, Launch launch) {
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t most = (((int64_t)1 << 32) - 1) / threads & ~(int64_t)7;
+    GemmArgs part = a;
+    for (int64_t at = 0; at < grid; at += most) {
+        part.first = (uint32_t)at;
+        launch(part, (unsigned)(grid - at < most ? grid - at : most));
+    }
+    return hipGetLastError();
+}
+
 template <int MT, int NT, int D>
 hipError_t launch_stream_t(const GemmArgs& a, hipStream_t stream) {
     const int64_t strips = (int64_t)a.NB * (kPanelTiles / NT);
     const int64_t grid = a.offsets ? strips * a.E : strips;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.offsets)
-        fp8_stream_kernel<MT, NT, D, true><<<(unsigned)grid, kStreamWaves * 64, 0, stream>>>(a);
-    else
-        fp8_stream_kernel<MT, NT, D, false><<<(unsigned)grid, kStreamWaves * 64, 0, stream>>>(a);
-    return hipGetLastError();
+    return launch_all(a, grid, kStreamWaves * 64, [&](const GemmArgs& p, unsigned n) {
+        if (a.offsets)
+            fp8_stream_kernel<MT, NT, D, true><<<n, kStreamWaves * 64, 0, stream>>>(p);
+        else
+            fp8_stream_kernel<MT, NT, D, false><<<n, kStreamWaves * 64, 0, stream>>>(p);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -437,8 +452,9 @@ fp8_tiled_kernel(GemmArgs a) {
     const int nbm = GROUPED ? count_row_tiles<BM>(a, lane) : a.nbm;
     const int64_t total = (int64_t)nbm * a.nbn * a.splits;
     const int64_t share = (total + 7) / 8;
-    int64_t task = (int64_t)(blockIdx.x & 7) * share + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= share || task >= total) return;
+    const uint32_t block = a.first + blockIdx.x;
+    int64_t task = (int64_t)(block & 7) * share + (block >> 3);
+    if ((block >> 3) >= share || task >= total) return;
     const int part = (int)(task % a.splits);
     const int64_t tile_id = task / a.splits;
     const int group = (int)(tile_id / ((int64_t)GM * a.nbn));
@@ -755,14 +771,14 @@ hipError_t launch_tiled_t(const GemmArgs& a, const Plan& p, hipStream_t stream) 
     if (p.bn != C::BN || p.bm != C::BM || (C::kAhead && (a.KB < 4 || a.splits > 1)))
         return hipErrorInvalidValue;
     const int64_t grid = (p.tiles * p.splits + 7) / 8 * 8;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (a.offsets)
-        fp8_tiled_kernel<WN, WM, NT, MT, STAGES, true>
-            <<<(unsigned)grid, C::kWaves * 64, C::kLds, stream>>>(a);
-    else
-        fp8_tiled_kernel<WN, WM, NT, MT, STAGES, false>
-            <<<(unsigned)grid, C::kWaves * 64, C::kLds, stream>>>(a);
-    return hipGetLastError();
+    return launch_all(a, grid, C::kWaves * 64, [&](const GemmArgs& q, unsigned n) {
+        if (a.offsets)
+            fp8_tiled_kernel<WN, WM, NT, MT, STAGES, true>
+                <<<n, C::kWaves * 64, C::kLds, stream>>>(q);
+        else
+            fp8_tiled_kernel<WN, WM, NT, MT, STAGES, false>
+                <<<n, C::kWaves * 64, C::kLds, stream>>>(q);
+    });
 }
 
 hipError_t launch_tiled(const GemmArgs& a, const Plan& p, hipStream_t stream) {

@@ -81,6 +81,7 @@ struct GemmArgs {
     int nbn, nbm;             // column tiles; row tiles (for groups: the most there can be)
     int splits;
     size_t s_off, z_off;
+    uint32_t first;           // workgroups of the call in earlier launches, a multiple of 8
 };
 
 // E = 0: one product; otherwise M rows over E experts.
