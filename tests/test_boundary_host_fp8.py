@@ -180,3 +180,23 @@ def test_scales_need_the_alignment_of_a_float(lib):
         assert lib.fp8_repack(FAKE, at(n), 1, 256, 128, FAKE, 1 << 30, None) == INV
         assert lib.rowquant_swiglu(FAKE, 256, FAKE, 256, FAKE, at(n), 4, 256, 0, None) == INV
         assert lib.rowquant_swiglu(FAKE, 256, FAKE, 256, FAKE, at(n), 4, 256, 0x10, None) == INV
+
+
+def test_a_split_pays_for_its_partial_tiles(lib):
+    """Large products whose partial tiles would make 100 to 210 MB are not split (they are
+    faster whole), and no shape of the range asks for more than the parts that still pay."""
+    from w4a16_dequant_gemm_amd import fp8
+    for M, N, K in ((1425, 11303, 18384), (2113, 7930, 22064), (4073, 1674, 28240),
+                    (2028, 8262, 16096)):
+        assert fp8.fp8_workspace_bytes(M, N, K) == 0
+    import random
+    rng = random.Random(3)
+    size = lambda low, high: int(low * (high / low) ** rng.random())    # noqa: E731
+    split = 0
+    for _ in range(4000):
+        M, N, K = size(1, 4096), size(64, 28672), size(16, 1792) * 16
+        need = fp8.fp8_workspace_bytes(M, N, K)
+        # parts beyond 16 MB cost 0.8 us a MB: 96 MB cost 64, more than a split can save
+        assert need <= 96 << 20, (M, N, K)
+        split += need > 0
+    assert split > 1000
