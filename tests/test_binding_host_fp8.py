@@ -105,3 +105,22 @@ def test_a_blob_of_another_layout_is_refused():
         packed.layout_version = fp8.FP8_LAYOUT_VERSION + 1
         with pytest.raises(w4.W4A16Error):
             call(packed)
+
+
+def test_workspace_sizes_are_kept_by_device_and_not_forever(monkeypatch):
+    asked = []
+
+    def need(M, N, K, *rest):
+        asked.append(M)
+        return 64 * M
+    monkeypatch.setattr(fp8, "fp8_workspace_bytes", need)
+    monkeypatch.setattr(w4, "w4a16_workspace_bytes", need)
+    monkeypatch.setattr(w4, "_ws_bytes", {})
+    for kept, ask in ((fp8._ws_bytes, lambda d, m: fp8._workspace_need(d, m, 128, 512, 0)),
+                      (w4._ws_bytes, lambda d, m: w4._workspace_need(d, m, 128, 512, 128, 0))):
+        asked.clear()
+        assert [ask(0, 5), ask(0, 5), ask(1, 5), ask(0, 5)] == [320] * 4
+        assert asked == [5, 5]                      # once per device
+        for m in range(20000):
+            assert ask(0, m) == 64 * m
+        assert len(kept) <= 4096

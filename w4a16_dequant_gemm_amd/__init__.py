@@ -216,13 +216,23 @@ def w4a16_workspace_bytes(M: int, N: int, K: int, group_size: int, flags: int) -
     return int(load_library().w4a16_workspace_bytes(M, N, K, group_size, flags))
 
 
-def _workspace_need(M, N, K, G, flags) -> int:
-    # the plan depends on the shape and the flags (plan hints included) only
-    key = (M, N, K, G, flags)
-    need = _ws_bytes.get(key)
+_WS_BYTES_KEPT = 4096
+
+
+def _kept_bytes(kept: dict, key, compute) -> int:
+    """compute(), or what it gave for this key.  The plan depends on the device, the shape and
+    the flags (plan hints included) only; the answers of a few thousand shapes are kept."""
+    need = kept.get(key)
     if need is None:
-        need = _ws_bytes[key] = w4a16_workspace_bytes(M, N, K, G, flags)
+        if len(kept) >= _WS_BYTES_KEPT:
+            kept.clear()
+        need = kept[key] = compute()
     return need
+
+
+def _workspace_need(device_index, M, N, K, G, flags) -> int:
+    return _kept_bytes(_ws_bytes, (device_index, M, N, K, G, flags),
+                       lambda: w4a16_workspace_bytes(M, N, K, G, flags))
 
 
 @dataclass
@@ -392,7 +402,7 @@ def w4a16_gemm(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
     flags = packed.flags if plan is None else packed.flags | plan_flags(plan)
     sh = _stream_handle(stream)
     if workspace is None:
-        need = _workspace_need(M, N, K, G, flags)
+        need = _workspace_need(X.get_device(), M, N, K, G, flags)
         if need:
             workspace = _workspace_at(need, X.get_device(), sh)
     else:
@@ -419,7 +429,8 @@ def w4a16_gemm_ex(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
     K, N, G = packed.K, packed.N, packed.group_size
     flags = packed.flags | plan_flags(plan)
     if workspace is None:
-        workspace = workspace_for(_workspace_need(M, N, K, G, flags), X.device, stream)
+        workspace = workspace_for(_workspace_need(X.get_device(), M, N, K, G, flags), X.device,
+                                  stream)
     else:
         _require_workspace(workspace, "w4a16_gemm_ex", X.get_device())
     _check(lib.w4a16_gemm_ex(_ptr(X), _ptr(packed.data), packed.data.numel(), _ptr(Y), M, N, K,

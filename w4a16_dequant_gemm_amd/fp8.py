@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _empty_on, _ptr, _require, _require_workspace, _stream,
+               _bad, _check, _empty_on, _kept_bytes, _ptr, _require, _require_workspace, _stream,
                _stream_handle, load_library, workspace_for)
 
 FP8_LAYOUT_VERSION = 1   # of include/fp8.h
@@ -127,13 +127,9 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
     return rows, K, *_DT[out]
 
 
-def _workspace_need(M: int, N: int, K: int, flags: int) -> int:
-    # the plan depends on the shape and the flags only
-    key = (M, N, K, flags)
-    need = _ws_bytes.get(key)
-    if need is None:
-        need = _ws_bytes[key] = fp8_workspace_bytes(M, N, K, flags)
-    return need
+def _workspace_need(device_index: int, M: int, N: int, K: int, flags: int) -> int:
+    return _kept_bytes(_ws_bytes, (device_index, M, N, K, flags),
+                       lambda: fp8_workspace_bytes(M, N, K, flags))
 
 
 def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "bf16",
@@ -151,7 +147,8 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
         _require(Y, "fp8_gemm: Y", tdt, M * N, xq.device)
     flags = flag if plan is None else flag | plan_flags_fp8(plan)
     if workspace is None:
-        workspace = workspace_for(_workspace_need(M, N, K, flags), xq.device, stream)
+        workspace = workspace_for(_workspace_need(xq.get_device(), M, N, K, flags), xq.device,
+                                  stream)
     else:
         _require_workspace(workspace, "fp8_gemm", xq.get_device())
     _check(_lib().fp8_gemm(xq.data_ptr(), xs.data_ptr(), packed.data.data_ptr(),
