@@ -117,9 +117,9 @@ __device__ __forceinline__ int offset_at(const GemmArgs& a, int e) {
 
 // ---------------------------------------------------------------------------
 // Streaming kernel (few rows per expert): the weights' bytes bound it.  A
-// workgroup owns NT neighbouring tiles (16 NT columns) of one expert; its 8
+// workgroup owns a tile (16 columns) of one expert; its 8
 // waves take the blocks of K in turn (wave w: kb = w, w + 8, ...: together 16
-// KiB of consecutive blob per step and tile), each wave with a ring of D blocks
+// KiB of consecutive blob per step), each wave with a ring of kStreamDepth blocks
 // in flight straight from memory to registers, and the 8 partial tiles add up
 // in LDS in wave order.  MT row tiles of 16 share each load of weights; more
 // rows than that are taken in turns.  Splitting K over the waves keeps all CUs
@@ -129,24 +129,26 @@ __device__ __forceinline__ int offset_at(const GemmArgs& a, int e) {
 // 8 rows the rows of X, read again by every workgroup, take as long as the weights
 // and the tiled kernel is ahead (16 rows: 55 against 45 us).
 // ---------------------------------------------------------------------------
-template <int MT, int NT, int D, bool GROUPED>
+constexpr int kStreamDepth = 4;
+
+template <int MT, bool GROUPED>
 __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs a) {
-    __shared__ f32x4 red[kStreamWaves][MT * NT][64];
+    constexpr int D = kStreamDepth;
+    __shared__ f32x4 red[kStreamWaves][MT][64];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int strips = a.NB * (kPanelTiles / NT);
+    const int strips = a.NB * kPanelTiles;
     const uint32_t block = a.first + blockIdx.x;
-    int e = 0, strip = block;
+    int e = 0, tile = block;   // the tile within the expert
     int64_t lo = 0, hi = a.M;
     if constexpr (GROUPED) {
         e = block / strips;
-        strip = block - e * strips;
+        tile = block - e * strips;
         lo = offset_at(a, e);
         hi = offset_at(a, e + 1);
     }
     if (lo >= hi) return;
-    const int tile = strip * NT;          // first tile, within the expert
     const int panel = tile / kPanelTiles;
     if (panel * kBlock + 4 * (tile % kPanelTiles) >= a.N) return;   // columns past N only
     const int KB = a.KB;
@@ -169,22 +171,17 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
             xsrc[t] = a.xq + r * a.K + 16 * g;
             xscale[t] = a.xs + r * KB;
         }
-        f32x4 acc[MT][NT];
+        f32x4 acc[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-        i32x4 wb[D][NT][2], xb[D][MT][2];
+        i32x4 wb[D][2], xb[D][MT][2];
         float sx[D][MT], sw[D];
         auto fill = [&](int slot, int step) __attribute__((always_inline)) {
             const int kb = wave + kStreamWaves * step;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const i32x4* p = (const i32x4*)(wsrc + ((size_t)j * KB + kb) * kChunkBytes);
-                wb[slot][j][0] = __builtin_nontemporal_load(p);
-                wb[slot][j][1] = __builtin_nontemporal_load(p + 64);
-            }
+            const i32x4* w = (const i32x4*)(wsrc + (size_t)kb * kChunkBytes);
+            wb[slot][0] = __builtin_nontemporal_load(w);
+            wb[slot][1] = __builtin_nontemporal_load(w + 64);
             sw[slot] = wscale[kb];
             const int left = a.K - kb * kBlock - 16 * g;   // bytes of the row from the lane's on
 #pragma unroll
@@ -209,34 +206,29 @@ __global__ __launch_bounds__(kStreamWaves * 64) void fp8_stream_kernel(GemmArgs 
                             b[t] = cat(xb[i][t][0], xb[i][t][1]);
                             s[t] = sx[i][t] * sw[i];
                         }
+                        const i32x8 w = cat(wb[i][0], wb[i][1]);
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const i32x8 w = cat(wb[i][j][0], wb[i][j][1]);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t)
-                                acc[t][j] = scaled_add(acc[t][j], block_sums(w, b[t]), s[t]);
-                        }
+                        for (int t = 0; t < MT; ++t)
+                            acc[t] = scaled_add(acc[t], block_sums(w, b[t]), s[t]);
                         if (base + i + D < n_steps) fill(i, base + i + D);
                     }
                 }
             }
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) red[wave][t * NT + j][lane] = acc[t][j];
+        for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
         __syncthreads();
-        for (int v = tid; v < MT * NT * 64; v += kStreamWaves * 64) {
-            const int tj = v >> 6, l = v & 63;
-            f32x4 y = red[0][tj][l];
+        for (int v = tid; v < MT * 64; v += kStreamWaves * 64) {
+            const int t = v >> 6, l = v & 63;
+            f32x4 y = red[0][t][l];
 #pragma unroll
-            for (int w = 1; w < kStreamWaves; ++w) y += red[w][tj][l];
-            const int64_t m = m0 + 16 * (tj / NT) + (l & 15);
+            for (int w = 1; w < kStreamWaves; ++w) y += red[w][t][l];
+            const int64_t m = m0 + 16 * t + (l & 15);
             if (m < hi) {
                 bool ok;
                 x_row<GROUPED>(a, m, ok);
                 if (!ok) y = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                const int n = panel * kBlock + 32 * (l >> 4) + 4 * (tile % kPanelTiles + tj % NT);
+                const int n = panel * kBlock + 32 * (l >> 4) + 4 * (tile % kPanelTiles);
                 store4(a.Y, m, n, a.N, y);
             }
         }
@@ -258,15 +250,15 @@ hipError_t launch_all(const GemmArgs& a, int64_t grid, int threads, Launch launc
     return hipGetLastError();
 }
 
-template <int MT, int NT, int D>
+template <int MT>
 hipError_t launch_stream_t(const GemmArgs& a, hipStream_t stream) {
-    const int64_t strips = (int64_t)a.NB * (kPanelTiles / NT);
+    const int64_t strips = (int64_t)a.NB * kPanelTiles;
     const int64_t grid = a.offsets ? strips * a.E : strips;
     return launch_all(a, grid, kStreamWaves * 64, [&](const GemmArgs& p, unsigned n) {
         if (a.offsets)
-            fp8_stream_kernel<MT, NT, D, true><<<n, kStreamWaves * 64, 0, stream>>>(p);
+            fp8_stream_kernel<MT, true><<<n, kStreamWaves * 64, 0, stream>>>(p);
         else
-            fp8_stream_kernel<MT, NT, D, false><<<n, kStreamWaves * 64, 0, stream>>>(p);
+            fp8_stream_kernel<MT, false><<<n, kStreamWaves * 64, 0, stream>>>(p);
     });
 }
 
@@ -794,8 +786,8 @@ hipError_t launch_tiled(const GemmArgs& a, const Plan& p, hipStream_t stream) {
 
 hipError_t launch(const GemmArgs& a, const Plan& p, hipStream_t stream) {
     if (p.variant == TILED) return launch_tiled(a, p, stream);
-    if (p.cfg == 1) return launch_stream_t<1, 1, 4>(a, stream);
-    return launch_stream_t<2, 1, 4>(a, stream);
+    if (p.cfg == 1) return launch_stream_t<1>(a, stream);
+    return launch_stream_t<2>(a, stream);
 }
 
 }  // namespace

@@ -20,8 +20,6 @@ import torch
 from . import (W4A16Error, W4A16_ERR_UNSUPPORTED, _bad, _check, _empty_on, _require,
                _stream_handle, load_library)
 
-ROWQUANT_KIND = {"fp8": 0x00, "int8": 0x10, "mx": 0x20, "x16": 0x30}
-ROWQUANT_MAX_ROW = 131072
 C_FUNCTIONS_ROWQUANT = ("rowquant_rmsnorm", "rowquant_swiglu")
 
 _F16, _BF16 = torch.float16, torch.bfloat16
