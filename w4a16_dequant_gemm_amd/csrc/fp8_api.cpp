@@ -200,8 +200,8 @@ GemmArgs make_args(const uint8_t* xq, const float* xs, const void* packed, const
     a.Y = Y;
     a.cnt = (uint32_t*)workspace;
     a.part = workspace ? (float*)((uint8_t*)workspace + kCounterBytes) : nullptr;
-    a.M = M;
-    a.T = T;
+    a.M = (int)M;
+    a.T = (int)T;
     a.N = (int)L.N;
     a.K = (int)L.K;
     a.KB = (int)L.KB;

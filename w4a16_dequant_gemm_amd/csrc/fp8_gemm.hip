@@ -112,7 +112,7 @@ __device__ __forceinline__ int64_t x_row(const GemmArgs& a, int64_t m, bool& ok)
 
 // Rows [lo, hi) of expert e, whatever offsets holds: both inside [0, M].
 __device__ __forceinline__ int offset_at(const GemmArgs& a, int e) {
-    return max(0, min(a.offsets[e], (int)a.M));
+    return max(0, min(a.offsets[e], a.M));
 }
 
 // ---------------------------------------------------------------------------
@@ -461,7 +461,7 @@ fp8_tiled_kernel(GemmArgs a) {
         if (rt.lo >= rt.hi) return;   // offsets that do not ascend
     } else {
         rt.lo = mb * BM;
-        rt.hi = (int)min((int64_t)rt.lo + BM, a.M);
+        rt.hi = min(rt.lo + BM, a.M);
     }
     const int tile0 = nb * (C::BN / 16);          // first operand tile of the workgroup
     const int tiles = a.NB * kPanelTiles;

@@ -76,13 +76,15 @@ struct GemmArgs {
     void* Y;
     uint32_t* cnt;            // split K: a counter per tile, then the partial tiles
     float* part;
-    int64_t M, T;             // rows of Y, rows of X
+    int M, T;                 // rows of Y, rows of X
     int N, K, KB, NB, E;
     int nbn, nbm;             // column tiles; row tiles (for groups: the most there can be)
     int splits;
-    size_t s_off, z_off;
     uint32_t first;           // workgroups of the call in earlier launches, a multiple of 8
+    size_t s_off, z_off;
 };
+// every line of arguments beyond costs each workgroup another scalar load's wait
+static_assert(sizeof(GemmArgs) <= 128, "the kernels' arguments fill two lines of 64 bytes");
 
 // E = 0: one product; otherwise M rows over E experts.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t E, uint32_t flags, int cus);
