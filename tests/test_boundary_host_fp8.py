@@ -200,3 +200,12 @@ def test_a_split_pays_for_its_partial_tiles(lib):
         assert need <= 96 << 20, (M, N, K)
         split += need > 0
     assert split > 1000
+
+
+@pytest.mark.parametrize("K,parts", [(4096, 8), (8208, 11)])
+def test_few_tiles_of_a_long_sum_are_split(lib, K, parts):
+    """16 tiles of 64 x 64 leave most of the chip idle unless K is split."""
+    from w4a16_dequant_gemm_amd import fp8
+    need = fp8.fp8_workspace_bytes(100, 512, K, fp8.plan_flags_fp8(("tiled", 3)))
+    assert need == 65536 + 2 * 8 * parts * 64 * 64 * 4
+    assert fp8.fp8_workspace_bytes(100, 512, K) > 0

@@ -428,3 +428,41 @@ def test_the_most_experts(plan):
         assert torch.equal(Y[at:at + 8192].float(), want)
     del packed, w, Y
     torch.cuda.empty_cache()
+
+
+# The 256 x 256 tile reads its scales four blocks at a time, the last group shifted back to
+# end in the row: blocks of K by every remainder of four.
+@pytest.mark.parametrize("K", [512, 640, 768, 896, 1104, 1248, 1392, 2032])
+def test_whole_numbers_are_exact_for_every_last_group_of_scales(K):
+    M, N = 260, 516
+    xq, xs, w, ws = make_exact(M, K, N, seed=K)
+    packed = f8().fp8_repack(w, ws)
+    want = product(values(xq, xs, True), values(w, ws, False))[0].half()
+    exq, exs, ew, ews = make_exact(M, K, N, E=3, seed=K + 1)
+    experts, off = f8().fp8_repack(ew, ews), offsets_of([3, 0, M - 3])
+    x = values(exq, exs, True)
+    ewant = torch.cat([product(x[:3], values(ew[0], ews[0], False))[0],
+                       product(x[3:], values(ew[2], ews[2], False))[0]]).half()
+    for plan in PLANS:
+        say(f"fp8 last group of scales K={K} plan={plan}")
+        Y = f8().fp8_gemm(xq, xs, packed, out="fp16", plan=plan)
+        assert torch.equal(Y, want), plan
+        Y = f8().fp8_grouped_gemm(exq, exs, experts, off, out="fp16", plan=plan)
+        assert torch.equal(Y, ewant), plan
+
+
+@pytest.mark.parametrize("K", [1024, 4096])
+def test_rows_do_not_depend_on_their_neighbours_in_tiles(K):
+    """... in whatever place of a tile, where both batches take the same parts of K."""
+    N = 256
+    xq, xs, w, ws = make(64, K, N, seed=18)
+    packed = f8().fp8_repack(w, ws)
+    for plan in PLANS[3:]:
+        flags = f8().plan_flags_fp8(plan)
+        if len({f8().fp8_workspace_bytes(M, N, K, flags) for M in (1, 64)}) > 1:
+            continue
+        say(f"neighbours K={K} plan={plan}")
+        whole = f8().fp8_gemm(xq, xs, packed, plan=plan)
+        for row in (0, 37, 63):
+            one = f8().fp8_gemm(xq[row:row + 1], xs[row:row + 1], packed, plan=plan)
+            assert torch.equal(one[0], whole[row]), (plan, row)

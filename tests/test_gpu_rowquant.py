@@ -480,3 +480,19 @@ def test_swiglu_of_more_rows_than_one_launch_holds(kind):
                 assert torch.equal(got[at].view(torch.uint8), ref.view(torch.uint8)), at
     del x, q, s
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("W", [32, 2048, 20480, 70016])
+def test_norm_in_place(kind, W):
+    """h may be x or the residual."""
+    x, r = rows(7, W, "bf16", 95), rows(7, W, "bf16", 96)
+    w = torch.ones(W, dtype=torch.bfloat16, device="cuda")
+    want = rq().rmsnorm_quantize_rows(x, w, residual=r, kind=kind)
+    say(f"norm in place {kind} W={W}")
+    for side in (0, 1):
+        pair = [x.clone(), r.clone()]
+        got = rq().rmsnorm_quantize_rows(pair[0], w, residual=pair[1], kind=kind, h=pair[side])
+        assert got[2] is pair[side]
+        for a, b in zip(got, want):
+            assert a is b is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
