@@ -88,8 +88,8 @@ double together(double a, double b, double c) {
 //   workgroup's reading of all partial tiles at 50 GB/s, or, if that takes longer, the way
 //   of all tiles' parts through memory and back at 2.5 TB/s, of which the caches take 16 MB (M
 //   = 1425, K = 18384, N = 11303 in 128 x 128 tiles: 500 us whole, 579, 620 and 720 in 2, 3 and
-//   4 parts; 450 in 256 x 256 tiles.  170 shapes whose plan this changed, against no such term:
-//   14% shorter in the mean, 6% longer at the worst).
+//   4 parts; 450 in 256 x 256 tiles.  67 shapes whose plan this term changes: 16% shorter
+//   in the mean, 6% longer at the worst).
 double tiled_us(const TileShape& t, double tiles, int splits, int64_t KB, double rows,
                 double weight_bytes, int cus, bool grouped) {
     const double steps = (double)((KB + splits - 1) / splits);

@@ -271,9 +271,12 @@ hipError_t launch_stream_t(const GemmArgs& a, hipStream_t stream) {
 // A stage: the weights' chunks as the blob holds them (a wave reads 64 x 16
 // consecutive bytes), and the rows of X of 128 bytes whose eight 16-byte pieces
 // are permuted by p ^ (row / 2) % 8 (the loads choose which global piece a lane
-// fetches, so that no two lanes of a read meet a bank twice).  The scales: 256
-// bytes per wave and stage, the first waves the rows', the others the panels'; or,
-// with two stages, four blocks of them per load.
+// fetches, so that no two lanes of a read meet a bank twice: the tiles of three stages
+// and more count no bank conflict).  The scales: 256 bytes per wave and stage, the
+// first waves the rows', the others the panels'; or, with two stages, four blocks of
+// them per load, whose reads (16 rows 16 bytes apart, two such sets per
+// instruction) are all that differs and make 29120 conflict cycles per CU of the
+// 1.6 million of 4096 rows at K = 8192, N = 28672.
 //
 // Two stages (the 256 x 256 tile, for many rows): see the loop's own comment.
 // It is bound by the matrix unit at the clock the power leaves it: 4096 rows, K =
@@ -282,7 +285,8 @@ hipError_t launch_stream_t(const GemmArgs& a, hipStream_t stream) {
 // Steps that led there, same sizes: one barrier per step and all loads at its start
 // 938, loads spread over the step and multiply-adds three tiles behind 892, the next
 // step's first operands read before its barrier 842, loads one in two tiles 820,
-// scales by fours 798.  Bringing lines into the L2 a step earlier cost 4%.
+// scales by fours 798.  Bringing lines into the L2 a step earlier cost 4%.  It takes all
+// 256 registers and spills one.
 //
 // More stages (smaller tiles, where the loads' latency counts): STAGES - 1 of them
 // in flight, one barrier per step, all operands of a step read at its start.
@@ -503,7 +507,8 @@ fp8_tiled_kernel(GemmArgs a) {
         sbase = (const float*)(a.blob + a.s_off) + (size_t)rt.e * a.NB * KB;
         srow = (uint32_t)min(tile0 / kPanelTiles + (lane & 1), a.NB - 1);
     }
-    const uint32_t ssrc = srow * (uint32_t)KB * 4u;   // below 2^36 / 32 bytes
+    // 2^30 rows of one block reach 2^32 - 4; rows of more blocks are fewer (X is below 2^36 bytes)
+    const uint32_t ssrc = srow * (uint32_t)KB * 4u;
 
     // Load q of the wave's kLoads of a stage.  In the last block of a K that is no
     // multiple of 128 the lanes past its end read zeros.
