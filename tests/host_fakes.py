@@ -18,7 +18,8 @@ class FakeTensor:
     device = torch.device("cuda", 0)
 
     def __init__(self, *shape, dtype, recorded=None):
-        self.shape, self.dtype, self.recorded = torch.Size(shape), dtype, recorded
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.recorded = [] if recorded is None else recorded   # streams it has to wait for
 
     def dim(self):
         return len(self.shape)

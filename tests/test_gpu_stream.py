@@ -117,3 +117,26 @@ def test_graphs_that_make_their_own_workspaces():
             got = f8().fp8_gemm(xq, xs, packed, stream=side)
             torch.cuda.synchronize()
             assert torch.equal(got, want)
+
+
+def test_inputs_dropped_while_another_stream_still_reads_them():
+    from w4a16_dequant_gemm_amd import rowquant
+    T, W = 512, 4096
+    kept = torch.randn(T, W, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    w = torch.ones(W, dtype=torch.bfloat16, device="cuda")
+    want = rowquant.rmsnorm_quantize_rows(kept, w)[:2]
+    big = torch.rand(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for rep in range(5):
+        say(f"inputs dropped, {rep}")
+        x = kept.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            keep_busy(big)
+        q, s, _ = rowquant.rmsnorm_quantize_rows(x, w, stream=side)
+        del x
+        junk = [torch.full_like(kept, float("nan")) for _ in range(4)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(q.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s, want[1])
+        del junk

@@ -78,7 +78,7 @@ def test_workspace_made_in_a_capture_serves_that_capture_alone(streams):
     assert w4._workspace_at(1 << 20, 0, 0x20) is outside
 
 
-def calls():
+def calls(fake=fake):
     """name -> (a call with `stream=`, how many outputs it makes)."""
     from w4a16_dequant_gemm_amd import fp8, mxfp4, rowquant, w4a8
     half, u8, f32, i8, i32 = (torch.float16, torch.uint8, torch.float32, torch.int8, torch.int32)
@@ -110,6 +110,15 @@ def calls():
     }
 
 
+def without_library(monkeypatch):
+    from w4a16_dequant_gemm_amd import fp8, mxfp4, rowquant, w4a8
+    monkeypatch.setattr(w4, "_lib", FakeLibrary())
+    for module in (fp8, rowquant, w4a8, mxfp4):
+        monkeypatch.setattr(module, "_lib", FakeLibrary)
+    monkeypatch.setattr(fp8, "_ws_bytes", {})
+    monkeypatch.setattr(w4, "_ws_bytes", {})
+
+
 NAMES = ["norm", "swiglu", "fp8_gemm", "fp8_grouped_gemm", "fp8_repack", "w4a16_gemm",
          "w4a16_gemm_ex", "w4a16_dequant", "w4a16_unrepack", "w4a8_quantize_rows", "w4a8_gemm",
          "w4a8_dequant", "mxfp4_quantize_rows", "mxfp4_gemm"]
@@ -119,7 +128,6 @@ NAMES = ["norm", "swiglu", "fp8_gemm", "fp8_grouped_gemm", "fp8_repack", "w4a16_
 @pytest.mark.parametrize("handle", [CURRENT, 0x20, 0])
 def test_outputs_are_made_on_the_stream_of_the_call(streams, monkeypatch, name, handle):
     """... and wait for torch's current stream too when they are dropped."""
-    from w4a16_dequant_gemm_amd import fp8, mxfp4, rowquant, w4a8
     call, outputs = calls()[name]
     made, recorded = [], []
 
@@ -130,11 +138,44 @@ def test_outputs_are_made_on_the_stream_of_the_call(streams, monkeypatch, name, 
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch, "empty_like", lambda like, dtype=None:
                         empty(like.shape, dtype=dtype or like.dtype))
-    monkeypatch.setattr(w4, "_lib", FakeLibrary())
-    for module in (fp8, rowquant, w4a8, mxfp4):
-        monkeypatch.setattr(module, "_lib", FakeLibrary)
-    monkeypatch.setattr(fp8, "_ws_bytes", {})
-    monkeypatch.setattr(w4, "_ws_bytes", {})
+    without_library(monkeypatch)
     call(handle)
     assert made == [handle] * outputs
     assert recorded == ([] if handle == CURRENT else [CURRENT] * outputs)
+
+
+class TorchStream:
+    """Stands in for torch.cuda.Stream."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_of_a_call_wait_for_its_stream_when_they_are_dropped(streams, monkeypatch, name):
+    """... but not for a raw handle, which its owner may have destroyed by then."""
+    monkeypatch.setattr(torch.cuda, "Stream", TorchStream)
+    without_library(monkeypatch)
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None:
+                        fake(*((shape,) if isinstance(shape, int) else shape), dtype=dtype))
+    monkeypatch.setattr(torch, "empty_like", lambda like, dtype=None:
+                        fake(*like.shape, dtype=dtype or like.dtype))
+    given = []
+
+    def kept(*shape, dtype):
+        given.append(FakeTensor(*shape, dtype=dtype))
+        return given[-1]
+    side = TorchStream(0x20)
+    call, _ = calls(kept)[name]
+    call(side)
+    used = [t for t in given if side in t.recorded]
+    assert len(used) >= 1 and all(t.recorded.count(side) <= 2 for t in used)
+    expect = {"norm": 2, "swiglu": 1, "fp8_gemm": 3, "fp8_grouped_gemm": 4, "fp8_repack": 2,
+              "w4a16_gemm": 2, "w4a16_gemm_ex": 2, "w4a16_dequant": 1, "w4a16_unrepack": 1,
+              "w4a8_quantize_rows": 1, "w4a8_gemm": 3, "w4a8_dequant": 1,
+              "mxfp4_quantize_rows": 1, "mxfp4_gemm": 3}
+    assert len(used) == expect[name]
+    given.clear()
+    call, _ = calls(kept)[name]
+    call(0x20)
+    assert not any(t.recorded for t in given)

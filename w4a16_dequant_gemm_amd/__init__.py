@@ -171,6 +171,16 @@ def _empty_on(stream, shape, dtype, device: torch.device) -> torch.Tensor:
     return t
 
 
+def _used_on(stream, *tensors):
+    """A call's tensors that are dropped before it has run keep their memory until `stream` is
+    through with them.  The owner of a raw handle may destroy it, so with one the tensors
+    are the caller's to keep."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _bad(where: str):
     raise W4A16Error(W4A16_ERR_INVALID_ARG, where)
 
@@ -268,6 +278,8 @@ def w4a16_repack(qweight: torch.Tensor, scales: torch.Tensor, zeros: Optional[to
     _check(load_library().w4a16_repack(_ptr(qweight), _ptr(scales), _ptr(zeros), K, N,
                                        group_size, flags, _ptr(packed), nbytes, _stream(stream)),
            "w4a16_repack")
+    if stream is not None:
+        _used_on(stream, qweight, scales, zeros)
     return PackedW4(packed, K, N, group_size, flags, w4a16_layout_version())
 
 
@@ -280,6 +292,8 @@ def w4a16_unrepack(packed: PackedW4, stream=None):
     _check(load_library().w4a16_unrepack(_ptr(packed.data), packed.data.numel(), _ptr(qweight),
                                          _ptr(scales), _ptr(zeros), K, N, G, flags,
                                          _stream(stream)), "w4a16_unrepack")
+    if stream is not None:
+        _used_on(stream, packed.data)
     return qweight, scales, zeros
 
 
@@ -412,6 +426,8 @@ def w4a16_gemm(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
                         0 if workspace is None else workspace.numel(), sh)
     if st:
         _check(st, "w4a16_gemm")
+    if stream is not None:
+        _used_on(stream, X, packed.data, Y, workspace)
     return Y
 
 
@@ -437,6 +453,8 @@ def w4a16_gemm_ex(X: torch.Tensor, packed: PackedW4, M: Optional[int] = None,
                              G, flags, None if ep is None else ctypes.byref(ep), _ptr(workspace),
                              0 if workspace is None else workspace.numel(), _stream(stream)),
            "w4a16_gemm_ex")
+    if stream is not None:
+        _used_on(stream, X, packed.data, Y, workspace, col_scale, bias, aux)
     return Y
 
 
@@ -458,6 +476,8 @@ def w4a16_gemm_noalloc(X: torch.Tensor, packed: PackedW4, Y: torch.Tensor,
                                   packed.flags | plan_flags(plan),
                                   None if ep is None else ctypes.byref(ep), _stream(stream)),
            "w4a16_gemm_noalloc")
+    if stream is not None:
+        _used_on(stream, X, packed.data, Y, col_scale, bias, aux)
     return Y
 
 
@@ -469,6 +489,8 @@ def w4a16_dequant(packed: PackedW4, W_out: Optional[torch.Tensor] = None,
     _check(load_library().w4a16_dequant(_ptr(packed.data), packed.data.numel(), _ptr(W_out), K,
                                         N, packed.group_size, packed.flags, _stream(stream)),
            "w4a16_dequant")
+    if stream is not None:
+        _used_on(stream, packed.data, W_out)
     return W_out
 
 
@@ -488,6 +510,8 @@ def w4a16_read_probe(buf: torch.Tensor, nbytes: Optional[int] = None,
         out = _empty_on(stream, w4a16_read_probe_out_bytes(), torch.uint8, buf.device)
     _check(lib.w4a16_read_probe(_ptr(buf), nbytes, _ptr(out), out.numel(), _stream(stream)),
            "w4a16_read_probe")
+    if stream is not None:
+        _used_on(stream, buf, out)
     return out
 
 
@@ -496,6 +520,8 @@ def w4a16_mfma_layout_probe(A: torch.Tensor, B: torch.Tensor, flags: int,
     D = _empty_on(stream, (32, 32), torch.float32, A.device)
     _check(load_library().w4a16_mfma_layout_probe(_ptr(A), _ptr(B), _ptr(D), flags,
                                                   _stream(stream)), "w4a16_mfma_layout_probe")
+    if stream is not None:
+        _used_on(stream, A, B)
     return D
 
 

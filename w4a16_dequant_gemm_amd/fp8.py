@@ -17,7 +17,7 @@ import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
                _bad, _check, _empty_on, _kept_bytes, _ptr, _require, _require_workspace, _stream,
-               _stream_handle, load_library, workspace_for)
+               _stream_handle, _used_on, load_library, workspace_for)
 
 FP8_LAYOUT_VERSION = 1   # of include/fp8.h
 FP8_BLOCK = 128
@@ -101,6 +101,8 @@ def fp8_repack(w: torch.Tensor, ws: torch.Tensor, stream=None) -> PackedFP8:
     packed = _empty_on(stream, nbytes, torch.uint8, w.device)
     _check(_lib().fp8_repack(_ptr(w), _ptr(ws), E, K, N, _ptr(packed), nbytes, _stream(stream)),
            "fp8_repack")
+    if stream is not None:
+        _used_on(stream, w, ws)
     return PackedFP8(packed, E, K, N, w.dim() == 3)
 
 
@@ -156,6 +158,8 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
                            None if workspace is None else workspace.data_ptr(),
                            0 if workspace is None else workspace.numel(),
                            _stream_handle(stream)), "fp8_gemm")
+    if stream is not None:
+        _used_on(stream, xq, xs, packed.data, Y, workspace)
     return Y
 
 
@@ -182,4 +186,6 @@ def fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, offs
                                    packed.data.numel(), offsets.data_ptr(),
                                    None if rows is None else rows.data_ptr(), Y.data_ptr(), R, T,
                                    E, N, K, flags, _stream_handle(stream)), where)
+    if stream is not None:
+        _used_on(stream, xq, xs, packed.data, offsets, rows, Y)
     return Y

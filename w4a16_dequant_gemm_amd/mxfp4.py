@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _empty_on, _ptr, _require, _stream, load_library)
+               _bad, _check, _empty_on, _ptr, _require, _stream, _used_on, load_library)
 
 MXFP4_LAYOUT_VERSION = 1
 MXFP4_PLAN = {"stream": 0x10, "tiled": 0x20}
@@ -75,6 +75,8 @@ def mxfp4_repack(qweight: torch.Tensor, ws: torch.Tensor, K: int, N: int, stream
     packed = _empty_on(stream, nbytes, torch.uint8, dev)
     _check(_lib().mxfp4_repack(_ptr(qweight), _ptr(ws), K, N, _ptr(packed), nbytes,
                                _stream(stream)), "mxfp4_repack")
+    if stream is not None:
+        _used_on(stream, qweight, ws)
     return PackedMX(packed, K, N)
 
 
@@ -91,6 +93,8 @@ def mxfp4_quantize_rows(X: torch.Tensor, stream=None):
     flags = 0x1 if X.dtype == torch.bfloat16 else 0x0
     _check(_lib().mxfp4_quantize_rows(_ptr(X), _ptr(xq), _ptr(xs), M, K, flags, _stream(stream)),
            "mxfp4_quantize_rows")
+    if stream is not None:
+        _used_on(stream, X)
     return xq, xs
 
 
@@ -113,4 +117,6 @@ def mxfp4_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedMX, out: str = 
         _bad("mxfp4_gemm: the blob is on another device")
     _check(_lib().mxfp4_gemm(_ptr(xq), _ptr(xs), _ptr(packed.data), packed.data.numel(), _ptr(Y),
                              M, N, K, flag | plan_flags_mx(plan), _stream(stream)), "mxfp4_gemm")
+    if stream is not None:
+        _used_on(stream, xq, xs, packed.data, Y)
     return Y

@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_UNSUPPORTED, _bad, _check, _empty_on, _require,
-               _stream_handle, load_library)
+               _stream_handle, _used_on, load_library)
 
 C_FUNCTIONS_ROWQUANT = ("rowquant_rmsnorm", "rowquant_swiglu")
 
@@ -122,6 +122,8 @@ def rmsnorm_quantize_rows(x: torch.Tensor, weight: torch.Tensor,
                                    weight.data_ptr(), eps, None if h is None else h.data_ptr(),
                                    q.data_ptr(), None if s is None else s.data_ptr(), T, W, flags,
                                    _stream_handle(stream)), where)
+    if stream is not None:
+        _used_on(stream, x, residual, weight, q, s, h)
     return q, s, h
 
 
@@ -137,4 +139,6 @@ def swiglu_quantize_rows(gate: torch.Tensor, up: torch.Tensor, kind: str = "fp8"
     _check(_lib().rowquant_swiglu(gate.data_ptr(), ldg, up.data_ptr(), ldu, q.data_ptr(),
                                   None if s is None else s.data_ptr(), T, W, flags,
                                   _stream_handle(stream)), where)
+    if stream is not None:
+        _used_on(stream, gate, up, q, s)
     return q, s

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _empty_on, _ptr, _require, _stream, load_library)
+               _bad, _check, _empty_on, _ptr, _require, _stream, _used_on, load_library)
 
 W4A8_LAYOUT_VERSION = 1
 W4A8_OUT = {"fp16": 0x0, "bf16": 0x1, "i32": 0x2}
@@ -88,6 +88,8 @@ def w4a8_repack(qweight: torch.Tensor, s8: torch.Tensor, a: torch.Tensor, sw: to
     packed = _empty_on(stream, nbytes, torch.uint8, dev)
     _check(_lib().w4a8_repack(_ptr(qweight), _ptr(s8), _ptr(a), _ptr(sw), K, N, group_size,
                               _ptr(packed), nbytes, _stream(stream)), "w4a8_repack")
+    if stream is not None:
+        _used_on(stream, qweight, s8, a, sw)
     return PackedW8(packed, K, N, group_size)
 
 
@@ -102,6 +104,8 @@ def w4a8_dequant(packed: PackedW8, stream=None) -> torch.Tensor:
     W = _empty_on(stream, (K, N), torch.int8, packed.data.device)
     _check(_lib().w4a8_dequant(_ptr(packed.data), packed.data.numel(), _ptr(W), K, N, G,
                                _stream(stream)), "w4a8_dequant")
+    if stream is not None:
+        _used_on(stream, packed.data)
     return W
 
 
@@ -121,6 +125,8 @@ def w4a8_quantize_rows(X: torch.Tensor, xq: Optional[torch.Tensor] = None,
     flags = W4A8_X["bf16" if X.dtype == torch.bfloat16 else "fp16"]
     _check(_lib().w4a8_quantize_rows(_ptr(X), _ptr(xq), _ptr(sx), M, K, flags, _stream(stream)),
            "w4a8_quantize_rows")
+    if stream is not None:
+        _used_on(stream, X, xq, sx)
     return xq, sx
 
 
@@ -145,4 +151,6 @@ def w4a8_gemm(xq: torch.Tensor, sx: Optional[torch.Tensor], packed: PackedW8, ou
     flags = W4A8_OUT[out] | plan_flags_w8(plan)
     _check(_lib().w4a8_gemm(_ptr(xq), _ptr(sx), _ptr(packed.data), packed.data.numel(), _ptr(Y),
                             M, N, K, packed.group_size, flags, _stream(stream)), "w4a8_gemm")
+    if stream is not None:
+        _used_on(stream, xq, sx, packed.data, Y)
     return Y
