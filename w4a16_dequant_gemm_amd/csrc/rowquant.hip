@@ -304,10 +304,10 @@ __global__ __launch_bounds__(THREADS) void row_kernel(RowArgs a) {
         sum = reduce_row<THREADS, false>(sum, part[0]);
         // IEEE square root and divisions: once per row
         float square = __fdiv_rn(sum, (float)a.W) + a.eps;
-        if (!(square >= 0x1p-80f && square < __builtin_inff())) {
+        if (BF16 && !(square >= 0x1p-80f && square < __builtin_inff())) {
             // the squares left fp32 (or what they lost there counts): once more with h
             // scaled by a power of two, which the quotient does not see.  The same
-            // for the whole workgroup.
+            // for the whole workgroup.  fp16's squares stay: 2^-48 to 2^34.
             const float k = square < 0x1p-80f ? 0x1p80f : 0x1p-80f;
             sum = 0.0f;
 #pragma unroll
