@@ -24,6 +24,9 @@ class FakeTensor:
     def dim(self):
         return len(self.shape)
 
+    def size(self, i):
+        return self.shape[i]
+
     def numel(self):
         return self.shape.numel()
 

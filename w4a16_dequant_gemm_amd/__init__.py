@@ -229,20 +229,21 @@ def w4a16_workspace_bytes(M: int, N: int, K: int, group_size: int, flags: int) -
 _WS_BYTES_KEPT = 4096
 
 
-def _kept_bytes(kept: dict, key, compute) -> int:
-    """compute(), or what it gave for this key.  The plan depends on the device, the shape and
-    the flags (plan hints included) only; the answers of a few thousand shapes are kept."""
-    need = kept.get(key)
-    if need is None:
-        if len(kept) >= _WS_BYTES_KEPT:
-            kept.clear()
-        need = kept[key] = compute()
+def _keep_bytes(kept: dict, key, need: int) -> int:
+    """Notes `need` under `key`; the answers of a few thousand shapes are kept."""
+    if len(kept) >= _WS_BYTES_KEPT:
+        kept.clear()
+    kept[key] = need
     return need
 
 
 def _workspace_need(device_index, M, N, K, G, flags) -> int:
-    return _kept_bytes(_ws_bytes, (device_index, M, N, K, G, flags),
-                       lambda: w4a16_workspace_bytes(M, N, K, G, flags))
+    # the plan depends on the device, the shape and the flags (plan hints included) only
+    key = (device_index, M, N, K, G, flags)
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = _keep_bytes(_ws_bytes, key, w4a16_workspace_bytes(M, N, K, G, flags))
+    return need
 
 
 @dataclass
@@ -384,7 +385,8 @@ def _gemm_args(where, X, packed, M, Y, stream, col_scale=None, bias=None, aux=No
     if packed.data.get_device() != dev_index:
         _bad(f"{where}: the blob is on {packed.data.device}, X on {X.device}")
     if Y is None:
-        Y = _empty_on(stream, (M, N), dt, X.device)
+        Y = (torch.empty((M, N), dtype=dt, device=X.device) if stream is None
+             else _empty_on(stream, (M, N), dt, X.device))
     elif (Y.dtype != dt or Y.numel() != M * N or not Y.is_contiguous() or not Y.is_cuda
           or Y.get_device() != dev_index):
         _require(Y, f"{where}: Y", dt, M * N, X.device)

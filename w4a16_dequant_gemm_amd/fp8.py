@@ -16,8 +16,8 @@ from typing import Optional
 import torch
 
 from . import (W4A16Error, W4A16_ERR_INVALID_ARG, W4A16_ERR_UNSUPPORTED, W4A16_PLAN_PARAM_SHIFT,
-               _bad, _check, _empty_on, _kept_bytes, _ptr, _require, _require_workspace, _stream,
-               _stream_handle, _used_on, load_library, workspace_for)
+               _bad, _check, _empty_on, _keep_bytes, _ptr, _require, _require_workspace, _stream,
+               _stream_handle, _used_on, _workspace_at, load_library)
 
 FP8_LAYOUT_VERSION = 1   # of include/fp8.h
 FP8_BLOCK = 128
@@ -122,7 +122,7 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
             or xs.get_device() != dev):
         _require(xs, f"{where}: xs", torch.float32, rows * kb, xq.device)   # raises
     # the same numbers the other way round, a row of scales per block, give another product
-    if xs.dim() != 1 and xs.shape[-1] != kb:
+    if xs.size(-1) != kb and xs.dim() != 1:
         _bad(f"{where}: xs is {tuple(xs.shape)}, its rows must hold {kb} scales")
     if packed.data.get_device() != dev:
         _bad(f"{where}: the blob is on another device")
@@ -130,8 +130,11 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
 
 
 def _workspace_need(device_index: int, M: int, N: int, K: int, flags: int) -> int:
-    return _kept_bytes(_ws_bytes, (device_index, M, N, K, flags),
-                       lambda: fp8_workspace_bytes(M, N, K, flags))
+    key = (device_index, M, N, K, flags)
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = _keep_bytes(_ws_bytes, key, fp8_workspace_bytes(M, N, K, flags))
+    return need
 
 
 def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "bf16",
@@ -144,20 +147,22 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out: str = "
         _bad("fp8_gemm: the blob holds experts")
     N = packed.N
     if Y is None:
-        Y = _empty_on(stream, (M, N), tdt, xq.device)
+        Y = (torch.empty((M, N), dtype=tdt, device=xq.device) if stream is None
+             else _empty_on(stream, (M, N), tdt, xq.device))
     else:
         _require(Y, "fp8_gemm: Y", tdt, M * N, xq.device)
     flags = flag if plan is None else flag | plan_flags_fp8(plan)
+    dev, handle = xq.get_device(), _stream_handle(stream)
     if workspace is None:
-        workspace = workspace_for(_workspace_need(xq.get_device(), M, N, K, flags), xq.device,
-                                  stream)
+        need = _workspace_need(dev, M, N, K, flags)
+        if need:
+            workspace = _workspace_at(need, dev, handle)
     else:
-        _require_workspace(workspace, "fp8_gemm", xq.get_device())
+        _require_workspace(workspace, "fp8_gemm", dev)
     _check(_lib().fp8_gemm(xq.data_ptr(), xs.data_ptr(), packed.data.data_ptr(),
                            packed.data.numel(), Y.data_ptr(), M, N, K, flags,
                            None if workspace is None else workspace.data_ptr(),
-                           0 if workspace is None else workspace.numel(),
-                           _stream_handle(stream)), "fp8_gemm")
+                           0 if workspace is None else workspace.numel(), handle), "fp8_gemm")
     if stream is not None:
         _used_on(stream, xq, xs, packed.data, Y, workspace)
     return Y
@@ -178,7 +183,8 @@ def fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, offs
         R = rows.numel()
         _require(rows, f"{where}: rows", torch.int32, R, xq.device)
     if Y is None:
-        Y = _empty_on(stream, (R, N), tdt, xq.device)
+        Y = (torch.empty((R, N), dtype=tdt, device=xq.device) if stream is None
+             else _empty_on(stream, (R, N), tdt, xq.device))
     else:
         _require(Y, f"{where}: Y", tdt, R * N, xq.device)
     flags = flag if plan is None else flag | plan_flags_fp8(plan)
