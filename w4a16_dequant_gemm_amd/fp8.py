@@ -122,7 +122,7 @@ def _rows(where: str, xq: torch.Tensor, xs: torch.Tensor, packed: PackedFP8, out
             or xs.get_device() != dev):
         _require(xs, f"{where}: xs", torch.float32, rows * kb, xq.device)   # raises
     # the same numbers the other way round, a row of scales per block, give another product
-    if xs.size(-1) != kb and xs.dim() != 1:
+    if xs.dim() > 1 and xs.size(-1) != kb:
         _bad(f"{where}: xs is {tuple(xs.shape)}, its rows must hold {kb} scales")
     if packed.data.get_device() != dev:
         _bad(f"{where}: the blob is on another device")

@@ -91,7 +91,7 @@ def _outputs(where: str, like: torch.Tensor, T: int, W: int, kind: str, q, s, st
         else:
             _require(s, f"{where}: s", s_dtype, T * (shape[1] if len(shape) == 2 else 1),
                      like.device)
-            if len(shape) == 2 and s.dim() != 1 and s.shape[-1] != shape[1]:
+            if len(shape) == 2 and s.dim() > 1 and s.size(-1) != shape[1]:
                 _bad(f"{where}: s is {tuple(s.shape)}, its rows must hold {shape[1]} scales")
     return q, s, flag | (0x1 if like.dtype == _BF16 else 0x0)
 
