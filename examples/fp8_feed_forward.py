@@ -5,8 +5,11 @@
 Four calls: the norm with the residual's addition ends in quantised rows, the first
 product gives the gate's and the up projection's columns side by side, the gated
 activation reads the two halves and ends in quantised rows, the second product gives y.
+Tokens of requests with a low-rank adapter get its part added to the first product's
+columns, read from the same quantised rows.
 By expert, the first product gathers each token's row for every expert it chose, and the
-rows stay in the experts' order.
+rows stay in the experts' order.  With a router's scores, its choice and order are one
+call ahead of the products, and the weighted sum back in the tokens' order one behind.
 
     python examples/fp8_feed_forward.py [--tokens 4096] [--hidden 4096] [--ffn 8192]
                                         [--experts 16] [--top 2]
@@ -19,7 +22,7 @@ import time
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from w4a16_dequant_gemm_amd import fp8, rowquant  # noqa: E402
+from w4a16_dequant_gemm_amd import fp8, lora, route, rowquant  # noqa: E402
 
 
 def quantise_weights(w):
@@ -45,10 +48,15 @@ class FeedForward:
     def _activation(self, both):
         return rowquant.swiglu_quantize_rows(both[:, :self.ffn], both[:, self.ffn:])
 
-    def dense(self, x, residual):
+    def dense(self, x, residual, adapters=None):
+        """adapters: (a [L][R][H], b [L][2F][R], ids int32 [T], scale [L])."""
         q, s, h = rowquant.rmsnorm_quantize_rows(x, self.norm_weight, residual=residual,
                                                  eps=self.eps)
-        q, s = self._activation(fp8.fp8_gemm(q, s, self.gate_up))
+        both = fp8.fp8_gemm(q, s, self.gate_up)
+        if adapters is not None:
+            a, b, ids, scale = adapters
+            lora.lora_add(both, q, a, b, ids, scale=scale, xs=s, out=both)
+        q, s = self._activation(both)
         return fp8.fp8_gemm(q, s, self.down), h
 
     def experts(self, x, residual, chosen, weight):
@@ -65,6 +73,16 @@ class FeedForward:
         back = torch.empty_like(y)
         back[order] = y
         return (back.view(*chosen.shape, -1).float() * weight[..., None]).sum(1).to(x.dtype), h
+
+    def routed(self, x, residual, logits, top):
+        """logits [T][E]: the router's scores; each token takes its top experts, weighted by
+        the softmax over them."""
+        r = route.route_tokens(logits, top)
+        q, s, h = rowquant.rmsnorm_quantize_rows(x, self.norm_weight, residual=residual,
+                                                 eps=self.eps)
+        q, s = self._activation(fp8.fp8_grouped_gemm(q, s, self.gate_up, r.offsets, rows=r.rows))
+        y = fp8.fp8_grouped_gemm(q, s, self.down, r.offsets)
+        return route.combine_rows(y, r.weights, r.places), h
 
 
 def reference(x, residual, norm_weight, gate_up, down, eps=1e-6):
@@ -90,15 +108,28 @@ def main():
 
     one = FeedForward(wn, gu[0], dn[0])
     many = FeedForward(wn, gu, dn)
-    weight, chosen = torch.randn(a.tokens, a.experts, device=d).softmax(1).topk(a.top, dim=1)
+    logits = torch.randn(a.tokens, a.experts, device=d)
+    weight, chosen = logits.softmax(1).topk(a.top, dim=1)
+    weight = weight / weight.sum(1, keepdim=True)
     n = min(a.tokens, 64)
     y, _ = one.dense(x, r)
     want = reference(x[:n], r[:n], wn, gu[0], dn[0])
     err = ((y[:n].float() - want).norm() / want.norm()).item()
     ye, _ = many.experts(x, r, chosen, weight)
+    yr, _ = many.routed(x, r, logits, a.top)
     wante = torch.stack([sum(weight[t, i] * reference(x[t:t + 1], r[t:t + 1], wn, gu[e], dn[e])[0]
                              for i, e in enumerate(chosen[t].tolist())) for t in range(min(n, 8))])
-    erre = ((ye[:len(wante)].float() - wante).norm() / wante.norm()).item()
+    erre, errr = (((z[:len(wante)].float() - wante).norm() / wante.norm()).item() for z in (ye, yr))
+    # four adapters of rank 16, each for runs of tokens; every fifth run has none
+    la = torch.randn(4, 16, a.hidden, device=d, dtype=dt) * a.hidden ** -0.5
+    lb = torch.randn(4, 2 * a.ffn, 16, device=d, dtype=dt) * 0.25 * a.hidden ** -0.5
+    ids = (torch.arange(a.tokens, device=d) // 16 % 5 - 1).to(torch.int32)
+    adapters = (la, lb, ids, torch.ones(4, device=d))
+    ya, _ = one.dense(x, r, adapters)
+    wanta = torch.cat([reference(x[t:t + 1], r[t:t + 1], wn,
+                                 gu[0] if i < 0 else gu[0].float() + lb[i].float() @ la[i].float(),
+                                 dn[0]) for t, i in enumerate(ids[:n].tolist())])
+    erra = ((ya[:n].float() - wanta).norm() / wanta.norm()).item()
 
     def us(f, reps=20):
         f()
@@ -112,9 +143,12 @@ def main():
     print(f"dense   {a.tokens} tokens {a.hidden} -> {a.ffn}: {us(lambda: one.dense(x, r)):.1f} us, "
           f"off by {err:.4f} of the fp32 block with unquantised weights")
     print(f"experts {a.tokens} tokens, {a.top} of {a.experts}: "
-          f"{us(lambda: many.experts(x, r, chosen, weight)):.1f} us, off by {erre:.4f}")
+          f"{us(lambda: many.experts(x, r, chosen, weight)):.1f} us, off by {erre:.4f}; with the "
+          f"router {us(lambda: many.routed(x, r, logits, a.top)):.1f} us, off by {errr:.4f}")
+    print(f"dense with adapters of 4 requests: {us(lambda: one.dense(x, r, adapters)):.1f} us, "
+          f"off by {erra:.4f}")
     # 8-bit rows and weights: 4 significant bits each, about 2.6% per operand in the norm
-    assert err < 0.08 and erre < 0.08
+    assert max(err, erre, errr, erra) < 0.08
 
 
 if __name__ == "__main__":

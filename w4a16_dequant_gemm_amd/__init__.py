@@ -148,6 +148,15 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(_stream_handle(stream))
 
 
+def _launch_stream(where: str, stream, device_index: int) -> int:
+    """hipStream_t for a call on tensors of device `device_index`, which must be the current
+    one: the library launches there."""
+    if torch._C._cuda_getDevice() != device_index:
+        _bad(f"{where}: the tensors are on device {device_index}, the current one is "
+             f"{torch._C._cuda_getDevice()}")
+    return _stream_handle(stream)
+
+
 def _on_stream(device_index: int, handle: int):
     """Context in which torch allocates and fills for the hipStream_t `handle`."""
     # a handle of 0 is the default stream; ExternalStream would take it for "any"
@@ -363,6 +372,16 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
     else:
         _workspaces[key] = ws
     return ws
+
+
+def _scratch(nbytes: int, device: torch.device, stream, handle: int) -> torch.Tensor:
+    """Memory for one call that needs no fill.  Calls on one stream follow one another and
+    share its workspace; a captured call gets memory of its own, since its graph may be
+    replayed beside another one, or beside calls on the stream it was captured from."""
+    if (torch._C._cuda_isCurrentStreamCapturing() if stream is None
+            else _capture_number(handle) is not None):
+        return _empty_on(stream, nbytes, torch.uint8, device)
+    return _workspace_at(nbytes, device.index, handle)
 
 
 _TORCH_DT = {0: torch.float16, W4A16_BF16: torch.bfloat16}

@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a16.so")
 HEADERS = ["w4a16_layout.h", "w4a16_device.h", "w4a16_internal.h", "w4a16_epilogue.h",
            "w4a8_internal.h", "w4a8_device.h", "mx_internal.h", "fp8_internal.h",
-           "rowquant_internal.h"]
+           "rowquant_internal.h", "math_device.h", "route_internal.h", "lora_internal.h"]
 
 COMMON = [
     "--offload-arch=gfx950",
@@ -59,6 +59,14 @@ UNITS = [
     ("rowquant_api.cpp", []),
     ("rowquant.hip", ["-DROWQUANT_TU_BF16=0"]),
     ("rowquant.hip", ["-DROWQUANT_TU_BF16=1"]),
+    ("route_api.cpp", []),
+    ("route.hip", ["-DROUTE_TU_TYPE=0"]),
+    ("route.hip", ["-DROUTE_TU_TYPE=1"]),
+    ("route.hip", ["-DROUTE_TU_TYPE=2"]),
+    ("combine.hip", []),
+    ("lora_api.cpp", []),
+    ("lora.hip", ["-DLORA_TU_BF16=0"]),
+    ("lora.hip", ["-DLORA_TU_BF16=1"]),
 ]
 
 

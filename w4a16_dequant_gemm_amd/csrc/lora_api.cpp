@@ -1,0 +1,110 @@
+// lora_api.cpp -- the extern "C" entry points declared in include/lora.h: host-side
+// validation (always before any HIP call), the plan and the launches.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/lora.h"
+#include "lora_internal.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 24;
+constexpr int64_t kMaxOut = (int64_t)1 << 37;
+
+bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+w4a16_status_t from_hip(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+w4a16_status_t check_shape(int64_t M, int64_t N, int64_t K, int64_t R, uint32_t flags) {
+    if (flags & ~(LORA_BF16 | LORA_X_FP8)) return W4A16_ERR_INVALID_ARG;
+    if (M < 0 || M >= kMaxDim || N < 1 || N >= kMaxDim || K < 1 || K >= kMaxDim || R < 1)
+        return W4A16_ERR_INVALID_ARG;
+    if (M * N >= kMaxOut) return W4A16_ERR_INVALID_ARG;
+    if (R % 8 || R > LORA_MAX_RANK || K % (flags & LORA_X_FP8 ? 16 : 8))
+        return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
+bool stride_ok(int64_t ld, int64_t W, int64_t M) {
+    return ld >= W && ld < ((int64_t)1 << 40) && (M < 2 || ld < ((int64_t)1 << 60) / M);
+}
+
+// The plan goes by the shape alone, so a row's sums are taken the same way whatever the
+// ids, and the workspace is known before the call.
+void set_plan(LoraArgs& a) {
+    const int steps = (int)ceil_div(a.K, kStep);
+    // first product: row tiles share the loads of A once there are workgroups enough
+    a.down_tiles = a.M >= 1024 ? (a.R <= 32 ? 4 : 2) : 1;
+    const int64_t groups = ceil_div(a.M, 16 * a.down_tiles);
+    const int64_t slices = ceil_div(a.R, a.R <= 16 ? 16 : a.R <= 32 ? 32 : 64);
+    a.splits = (int32_t)std::min<int64_t>({std::max<int64_t>(1, 512 / (groups * slices)),
+                                           ceil_div(steps, kDownWaves), 16});
+    const int64_t most = std::min<int64_t>(16 * a.down_tiles, std::min<int64_t>(a.L, a.M));
+    a.down_z = (int32_t)std::clamp<int64_t>(1024 / (groups * slices * a.splits), 1, most);
+    // second product
+    a.up_tiles = a.M < 512 ? 1 : a.R <= 64 ? 4 : a.R <= 128 ? 2 : 1;
+    const int64_t rows = ceil_div(a.M, 16 * a.up_tiles), runs = ceil_div(a.N, kUpCols);
+    a.up_each = (int32_t)std::clamp<int64_t>(rows * runs / 8192, 1, 4);
+    if (a.N >= (int64_t)1 << 23) a.up_each = 4;   // the grid's second dimension stays below 2^16
+    const int64_t waves = rows * ceil_div(runs, a.up_each);
+    a.up_z = (int32_t)std::clamp<int64_t>(
+        32768 / waves, 1, std::min<int64_t>(16 * a.up_tiles, std::min<int64_t>(a.L, a.M)));
+}
+
+size_t bytes_of(const LoraArgs& a) {
+    return (size_t)kSkip + (size_t)a.splits * (size_t)a.M * (size_t)a.R * 4;
+}
+
+}  // namespace
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, uint32_t flags) {
+    if (check_shape(M, N, K, R, flags) != W4A16_OK || M == 0) return 0;
+    LoraArgs a{};
+    a.M = M, a.N = N, a.K = K, a.R = (int32_t)R, a.L = 1;
+    set_plan(a);
+    return bytes_of(a);
+}
+
+w4a16_status_t lora_add(const void* base, int64_t ldb, const void* x, int64_t ldx,
+                        const float* xs, const void* a_weights, const void* b_weights,
+                        const float* scale, const int32_t* ids, void* out, int64_t ldo, int64_t M,
+                        int64_t N, int64_t K, int64_t R, int64_t L, uint32_t flags,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    const w4a16_status_t st = check_shape(M, N, K, R, flags);
+    if (st != W4A16_OK) return st;
+    const bool fp8 = (flags & LORA_X_FP8) != 0;
+    if (L < 1 || L >= kMaxDim || !stride_ok(ldb, N, M) || !stride_ok(ldo, N, M) ||
+        !stride_ok(ldx, K, M) || (M > 1 && ldx % (fp8 ? 16 : 8)) || fp8 != (xs != nullptr))
+        return W4A16_ERR_INVALID_ARG;
+    if (M == 0) return W4A16_OK;
+    if (!base || !x || !a_weights || !b_weights || !ids || !out || !aligned(base, 2) ||
+        !aligned(out, 2) || !aligned(x, 16) || !aligned(a_weights, 16) ||
+        !aligned(b_weights, 16) || !aligned(xs, 4) || !aligned(scale, 4) || !aligned(ids, 4) ||
+        (out == base && ldo != ldb))
+        return W4A16_ERR_INVALID_ARG;
+    LoraArgs a{};
+    a.base = base, a.x = x, a.xs = xs, a.a = a_weights, a.b = b_weights, a.scale = scale;
+    a.ids = ids, a.out = out;
+    a.ldb = ldb, a.ldx = ldx, a.ldo = ldo, a.M = M, a.N = N, a.K = K;
+    a.R = (int32_t)R, a.L = (int32_t)L, a.KB = (int32_t)ceil_div(K, 128);
+    set_plan(a);
+    if (!workspace || workspace_bytes < bytes_of(a)) return W4A16_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return W4A16_ERR_INVALID_ARG;
+    a.h = (float*)((uint8_t*)workspace + kSkip);
+    return from_hip(flags & LORA_BF16 ? launch_bf16(a, fp8, (hipStream_t)stream)
+                                      : launch_f16(a, fp8, (hipStream_t)stream));
+}
+
+}  // extern "C"
