@@ -67,97 +67,103 @@ __device__ __forceinline__ int row_id(const LoraArgs& a, int64_t row0, int rows,
 }
 
 // ---------------------------------------------------------------------------
-// First product.  Workgroup: RT tiles of 16 rows, RG groups of 16 ranks, one part of K
-// whose steps its waves take in turn; the waves' sums meet in LDS.  A lane's operands
-// are runs of 32 consecutive indices of K, in the same order on both sides.
+// First product.  Workgroup: 16 rows, RG groups of 16 ranks, one part of K whose steps its waves take in turn; the waves' sums meet in LDS.  The indices of a step
+// are dealt so that a load takes 64 consecutive bytes of each of its 16 rows.
 // ---------------------------------------------------------------------------
 
-template <bool FP8, int RT, int RG>
-struct Step {
-    u32x4 x[RT][FP8 ? 2 : 4];
-    u32x4 a[RG][4];
-    float s[RT];
+// First index of operand i of lane group g within a step, the same on both sides; E4M3
+// rows are loaded 16 codes at a time, which make two operands.
+template <bool FP8>
+__device__ __forceinline__ int index_of(int i, int g) {
+    return FP8 ? i / 2 * 64 + g * 16 + i % 2 * 8 : i * 32 + g * 8;
+}
+
+template <bool FP8>
+struct Rows {
+    u32x4 x[FP8 ? 2 : 4];
+    float s;
 };
 
-template <bool FP8, int RT, int RG>
-__device__ __forceinline__ void load_step(Step<FP8, RT, RG>& st, const LoraArgs& args,
-                                          const uint8_t* const (&x)[RT],
-                                          const float* const (&xs)[RT],
-                                          const uint16_t* const (&a)[RG], int step, int g) {
-    const int64_t k = (int64_t)step * kStep + g * 32;
-    const bool whole = (int64_t)(step + 1) * kStep <= args.K;   // the same for the wave
-    const u32x4 zeros = {0u, 0u, 0u, 0u};
+// WHOLE: all of the step lies inside K.
+template <bool FP8, bool WHOLE>
+__device__ __forceinline__ void load_rows(Rows<FP8>& st, int64_t K, const uint8_t* x,
+                                          const float* xs, int step, int g) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int i = 0; i < (FP8 ? 2 : 4); ++i) {
-            const int64_t at = k + i * (FP8 ? 16 : 8);
-            st.x[rt][i] = whole || at < args.K ? *(const u32x4*)(x[rt] + at * (FP8 ? 1 : 2)) : zeros;
-        }
-        if constexpr (FP8) st.s[rt] = xs[rt][step];
+    for (int i = 0; i < (FP8 ? 2 : 4); ++i) {
+        const int64_t at = (int64_t)step * kStep + index_of<FP8>(FP8 ? 2 * i : i, g);
+        st.x[i] = u32x4{0u, 0u, 0u, 0u};
+        if (WHOLE || at < K) st.x[i] = *(const u32x4*)(x + at * (FP8 ? 1 : 2));
     }
+    if constexpr (FP8) st.s = xs[step];
+}
+
+template <bool FP8, int RG, bool WHOLE>
+__device__ __forceinline__ void load_ranks(u32x4 (&w)[RG][4], int64_t K,
+                                           const uint16_t* const (&a)[RG], int step, int g) {
 #pragma unroll
     for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st.a[rg][i] = whole || k + i * 8 < args.K ? *(const u32x4*)(a[rg] + k + i * 8) : zeros;
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = (int64_t)step * kStep + index_of<FP8>(i, g);
+            w[rg][i] = u32x4{0u, 0u, 0u, 0u};
+            if (WHOLE || at < K) w[rg][i] = *(const u32x4*)(a[rg] + at);
+        }
 }
 
-template <bool FP8, int RT, int RG>
-__device__ __forceinline__ void use_step(f32x4 (&acc)[RT][RG], const Step<FP8, RT, RG>& st) {
+template <bool FP8, int RG>
+__device__ __forceinline__ void use_step(f32x4 (&acc)[RG], const Rows<FP8>& st,
+                                         const u32x4 (&w)[RG][4]) {
+    u32x4 x[4];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        u32x4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (FP8) {
-                const u32x4 q = st.x[rt][i / 2];
-                const uint32_t w0 = q[i % 2 * 2], w1 = q[i % 2 * 2 + 1];
-                x[i] = u32x4{widen<false>(w0), widen<true>(w0), widen<false>(w1), widen<true>(w1)};
-            } else {
-                x[i] = st.x[rt][i];
-            }
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (FP8) {
+            const u32x4 q = st.x[i / 2];
+            const uint32_t w0 = q[i % 2 * 2], w1 = q[i % 2 * 2 + 1];
+            x[i] = u32x4{widen<false>(w0), widen<true>(w0), widen<false>(w1), widen<true>(w1)};
+        } else {
+            x[i] = st.x[i];
         }
+    }
+    f32x4 c[RG];
 #pragma unroll
-        for (int rg = 0; rg < RG; ++rg) {
-            f32x4 c = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[rt][rg];
+    for (int rg = 0; rg < RG; ++rg) c[rg] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[rg];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c = mfma(st.a[rg][i], x[i], c);
-            if constexpr (FP8) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[rt][rg][i] = __builtin_fmaf(c[i], st.s[rt], acc[rt][rg][i]);
-            } else {
-                acc[rt][rg] = c;
-            }
+        for (int rg = 0; rg < RG; ++rg) c[rg] = mfma(w[rg][i], x[i], c[rg]);
+#pragma unroll
+    for (int rg = 0; rg < RG; ++rg) {
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[rg][i] = __builtin_fmaf(c[rg][i], st.s, acc[rg][i]);
+        } else {
+            acc[rg] = c[rg];
         }
     }
 }
 
-template <bool FP8, int RT, int RG>
+constexpr int kAhead = 4;   // steps of x in flight: it comes from HBM, the adapter from the L2
+
+template <bool FP8, int RG>
 __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
-    __shared__ f32x4 part[kDownWaves][RT * RG][64];
+    __shared__ f32x4 part[kDownWaves][RG][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, g = lane >> 4;
-    const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
+    const int64_t row0 = (int64_t)blockIdx.x * 16;
     const int slices = (args.R + 16 * RG - 1) / (16 * RG);
     const int split = blockIdx.y / slices, rank0 = blockIdx.y % slices * (16 * RG);
     const int steps = (int)((args.K + kStep - 1) / kStep);
     const int from = (int)((int64_t)steps * split / args.splits);
     const int to = (int)((int64_t)steps * (split + 1) / args.splits);
+    const int whole = min(to, (int)(args.K / kStep));
 
-    const int id = row_id(args, row0, 16 * RT, lane);
+    const int id = row_id(args, row0, 16, lane);
     unsigned long long todo = __ballot(id >= 0);
     if (todo == 0) return;
 
-    const uint8_t* x[RT];
-    const float* xs[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int64_t row = min(row0 + rt * 16 + col, args.M - 1);
-        x[rt] = (const uint8_t*)args.x + row * args.ldx * (FP8 ? 1 : 2);
-        xs[rt] = FP8 ? args.xs + row * args.KB : nullptr;
-    }
+    const int64_t row = min(row0 + col, args.M - 1);
+    const uint8_t* x = (const uint8_t*)args.x + row * args.ldx * (FP8 ? 1 : 2);
+    const float* xs = FP8 ? args.xs + row * args.KB : nullptr;
     for (int turn = 0; todo; ++turn) {   // every turn clears a bit
         const int adapter = __builtin_amdgcn_readlane(id, __ffsll(todo) - 1);
         const unsigned long long same = __ballot(id == adapter);
@@ -170,42 +176,53 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
             const int rank = min(rank0 + rg * 16 + col, args.R - 1);
             a[rg] = (const uint16_t*)args.a + ((int64_t)adapter * args.R + rank) * args.K;
         }
-        f32x4 acc[RT][RG] = {};
+        f32x4 acc[RG] = {};
+        Rows<FP8> ring[kAhead];
+        u32x4 w[2][RG][4];
         int step = from + wave;
-        if (step < to) {
-            Step<FP8, RT, RG> now, next;
-            load_step<FP8, RT, RG>(now, args, x, xs, a, step, g);
-            for (; step + kDownWaves < to; step += kDownWaves) {
-                load_step<FP8, RT, RG>(next, args, x, xs, a, step + kDownWaves, g);
-                use_step<FP8, RT, RG>(acc, now);
-                now = next;
+        if (step < whole) load_ranks<FP8, RG, true>(w[0], args.K, a, step, g);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (step + j * kDownWaves < whole)
+                load_rows<FP8, true>(ring[j], args.K, x, xs, step + j * kDownWaves, g);
+        while (step < whole) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (step + kDownWaves < whole)
+                    load_ranks<FP8, RG, true>(w[(j + 1) & 1], args.K, a, step + kDownWaves, g);
+                use_step<FP8, RG>(acc, ring[j], w[j & 1]);
+                if (step + kAhead * kDownWaves < whole)
+                    load_rows<FP8, true>(ring[j], args.K, x, xs, step + kAhead * kDownWaves, g);
+                step += kDownWaves;
+                if (step >= whole) break;
             }
-            use_step<FP8, RT, RG>(acc, now);
+        }
+        if (step < to) {   // K ends inside this step
+            load_rows<FP8, false>(ring[0], args.K, x, xs, step, g);
+            load_ranks<FP8, RG, false>(w[0], args.K, a, step, g);
+            use_step<FP8, RG>(acc, ring[0], w[0]);
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int rg = 0; rg < RG; ++rg) part[wave][rt * RG + rg][lane] = acc[rt][rg];
+        for (int rg = 0; rg < RG; ++rg) part[wave][rg][lane] = acc[rg];
         __syncthreads();
-        for (int i = threadIdx.x; i < RT * RG * 64; i += kDownWaves * 64) {
-            const int tile = i / 64, rt = tile / RG, rg = tile % RG;
-            f32x4 sum = part[0][tile][i & 63];
+        if (wave < RG) {
+            f32x4 sum = part[0][wave][lane];
 #pragma unroll
-            for (int w = 1; w < kDownWaves; ++w) sum += part[w][tile][i & 63];
+            for (int w = 1; w < kDownWaves; ++w) sum += part[w][wave][lane];
             // a lane's numbers are 4 consecutive ranks of one row
-            const int r = rt * 16 + (i & 15), rank = rank0 + rg * 16 + (i >> 4 & 3) * 4;
-            if ((same >> r & 1) && rank < args.R)
-                *(f32x4*)(args.h + ((int64_t)split * args.M + row0 + r) * args.R + rank) = sum;
+            const int rank = rank0 + wave * 16 + g * 4;
+            if ((same >> col & 1) && rank < args.R)
+                *(f32x4*)(args.h + ((int64_t)split * args.M + row0 + col) * args.R + rank) = sum;
         }
         __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------------------
-// Second product.  Wave: RT tiles of 16 rows and runs of 64 columns.  h is split into a
-// high and a low part of 16 bits each, so that the matrix instruction loses nothing that
-// the output could hold.  The columns are dealt so that a lane ends with 16 consecutive
-// ones of one row.
+// Second product.  Wave: 16 rows and runs of 64 columns, in order; the waves of a workgroup
+// lie side by side in rows where there are many, so that they find the adapter's numbers
+// in the L1.  h is split into a high and a low part of 16 bits each, so that the matrix
+// instruction loses nothing that the output could hold.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
@@ -227,167 +244,603 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4& high, u32x4& 
     }
 }
 
-// out[n ..] = base[n ..] + v for 8 columns, those behind N left out.
-__device__ __forceinline__ void add8(const uint16_t* base, uint16_t* out, int64_t n, int64_t N,
-                                     const float (&v)[8]) {
-    if (n + 8 <= N) {
-        const u32x4 q = *(const u32x4_any*)(base + n);
-        u32x4 y;
+// A row's h (lane group g: every fourth run of 8 ranks) into operands, splits of a number
+// four at a time; returns what the product has to be multiplied by.
+template <int KH>
+__device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[KH],
+                                               const LoraArgs& args, int64_t row, int adapter,
+                                               int g) {
+    const float scale = args.scale ? args.scale[adapter] : 1.0f;
+    float v[KH][8], most = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y[i] = to_half(to_float(q[i] & 0xFFFFu) + v[2 * i]) |
-                   to_half(to_float(q[i] >> 16) + v[2 * i + 1]) << 16;
-        *(u32x4_any*)(out + n) = y;
-    } else {
+    for (int kh = 0; kh < KH; ++kh) {
+        const int rank = (kh * 4 + g) * 8;
+        f32x4 p = {}, q = {};
+        if (rank < args.R) {
+            const float* h = args.h + row * args.R + rank;
+            const int64_t next = args.M * args.R;
+            int s = 0;
+            for (; s + 4 <= args.splits; s += 4) {
+                f32x4 a[4], c[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (n + i < N) out[n + i] = (uint16_t)to_half(to_float(base[n + i]) + v[i]);
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = *(const f32x4*)(h + (s + i) * next);
+                    c[i] = *(const f32x4*)(h + (s + i) * next + 4);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p += a[i], q += c[i];
+            }
+            for (; s < args.splits; ++s) {
+                p += *(const f32x4*)(h + s * next);
+                q += *(const f32x4*)(h + s * next + 4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[kh][i] = (i < 4 ? p[i] : q[i - 4]) * scale;
+            most = fmaxf(most, fabsf(v[kh][i]));
+        }
+    }
+    float back = 1.0f;
+    if constexpr (!BF16) {
+        // a row's numbers by a power of two to below 2^14, where neither part leaves
+        // fp16's range
+        most = fmaxf(most, __shfl_xor(most, 16, 64));
+        most = fmaxf(most, __shfl_xor(most, 32, 64));
+        const int e = (int)(__float_as_uint(most) >> 23) - 127;   // 128: not finite
+        const int shift = e == 128 ? 0 : min(13 - e, 120);
+        const float by = __uint_as_float((uint32_t)(127 + shift) << 23);
+        back = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll
+        for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[kh][i] *= by;
+    }
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh) split8(v[kh], high[kh], low[kh]);
+    return back;
+}
+
+// Columns n .. n+7 of a row of N, where it may end; those behind are zeros.
+__device__ __forceinline__ u32x4 load_end(const uint16_t* row, int64_t n, int64_t N) {
+    u32x4 q = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n + i < N) q[i / 2] |= (uint32_t)row[n + i] << (16 * (i & 1));
+    return q;
+}
+
+__device__ __forceinline__ void store_end(uint16_t* row, int64_t n, int64_t N, u32x4 q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n + i < N) row[n + i] = (uint16_t)(q[i / 2] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ u32x4 add8(u32x4 q, f32x4 low, f32x4 high, float by) {
+    u32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v0 = i < 2 ? low[2 * i] : high[2 * i - 4];
+        const float v1 = i < 2 ? low[2 * i + 1] : high[2 * i - 3];
+        y[i] = to_half(__builtin_fmaf(v0, by, to_float(q[i] & 0xFFFFu))) |
+               to_half(__builtin_fmaf(v1, by, to_float(q[i] >> 16))) << 16;
+    }
+    return y;
+}
+
+// The adapter's numbers for 64 columns from n0.  The matrix instruction's rows are dealt so
+// that a lane's results are 8 consecutive columns of each half (`column`).  WHOLE: all
+// columns lie inside N.  Operands behind R hold any of the row's numbers.
+template <int KH, bool WHOLE>
+__device__ __forceinline__ void load_adapter(u32x4 (&w)[4][KH], const uint16_t* b, int64_t n0,
+                                             int64_t N, int R, int col, int g) {
+    const uint16_t* run = b + n0 * R;   // the same for the wave
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        int n = t / 2 * 32 + col / 4 * 8 + t % 2 * 4 + col % 4;
+        if (!WHOLE) n = (int)min((int64_t)n, N - 1 - n0);
+#pragma unroll
+        for (int kh = 0; kh < KH; ++kh) {
+            const int rank = kh + 1 < KH ? (kh * 4 + g) * 8 : min((kh * 4 + g) * 8, R - 8);
+            w[t][kh] = *(const u32x4*)((const uint8_t*)run + (uint32_t)(n * R + rank) * 2u);
+        }
     }
 }
 
-// KH: operands of 32 ranks
-template <int RT, int KH>
-__global__ __launch_bounds__(kUpWaves * 64) void up_kernel(LoraArgs args) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = lane & 15, g = lane >> 4;
-    const int64_t row0 = (int64_t)blockIdx.x * (16 * RT);
-    const int64_t run0 = ((int64_t)blockIdx.y * kUpWaves + wave) * args.up_each;
-    const int64_t n_end = min((run0 + args.up_each) * kUpCols, args.N);
+// First of the lane's 8 consecutive columns of a half.
+__device__ __forceinline__ int column(int half, int g) { return half * 32 + g * 8; }
 
-    const int id = row_id(args, row0, 16 * RT, lane);
-    const unsigned long long with = __ballot(id >= 0);
-    if (blockIdx.z == 0 && args.out != args.base) {   // rows without an adapter
-        for (int r = 0; r < 16 * RT && row0 + r < args.M; ++r) {
-            if (with >> r & 1) continue;
-            const uint16_t* from = (const uint16_t*)args.base + (row0 + r) * args.ldb;
-            uint16_t* to = (uint16_t*)args.out + (row0 + r) * args.ldo;
-            for (int64_t n = run0 * kUpCols + lane; n < n_end; n += 64) to[n] = from[n];
-        }
+template <bool WHOLE>
+__device__ __forceinline__ void load_base(u32x4 (&y)[2], const uint16_t* base, int64_t n0, int64_t N,
+                                          int g) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+        y[half] = WHOLE ? u32x4(*(const u32x4_any*)(base + n0 + column(half, g)))
+                        : load_end(base, n0 + column(half, g), N);
+}
+
+template <int KH>
+__device__ __forceinline__ void multiply(f32x4 (&d)[4], u32x4 (&w)[4][KH], const u32x4 (&high)[KH],
+                                         const u32x4 (&low)[KH], int R, int g) {
+    const uint32_t keep = ((KH - 1) * 4 + g) * 8 < R ? ~0u : 0u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        w[t][KH - 1] &= keep;
+        d[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    unsigned long long todo = with;
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) d[t] = mfma(w[t][kh], high[kh], d[t]);
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) d[t] = mfma(w[t][kh], low[kh], d[t]);
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void add_run(const f32x4 (&d)[4], const u32x4 (&y)[2], float back,
+                                        uint16_t* out, bool mine, int64_t n0, int64_t N, int g) {
+    if (!mine) return;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const u32x4 q = add8(y[half], d[half * 2], d[half * 2 + 1], back);
+        if constexpr (WHOLE) *(u32x4_any*)(out + n0 + column(half, g)) = q;
+        else store_end(out, n0 + column(half, g), N, q);
+    }
+}
+
+constexpr int kRing = 2;   // runs of base in flight
+
+// KH: operands of 32 ranks; R is above 32 (KH - 1).
+template <int KH>
+__global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraArgs args) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int wide = args.up_wide;   // waves side by side in rows: 4 or 1
+    const int64_t row0 = ((int64_t)blockIdx.x * wide + wave % wide) * 16;
+    const int64_t part = (int64_t)blockIdx.y * (kUpWaves / wide) + wave / wide;
+    const int64_t first = part * args.up_each * kUpCols;
+    const int64_t end = min(args.N, first + (int64_t)args.up_each * kUpCols);
+    const int64_t whole = min(end, args.N / kUpCols * kUpCols);   // a run from here on ends inside
+    if (row0 >= args.M || first >= end) return;
+
+    const int id = row_id(args, row0, 16, lane);
+    unsigned long long todo = __ballot(id >= 0);
+    if (blockIdx.z == 0 && args.out != args.base && !(todo >> col & 1) && row0 + col < args.M) {
+        // rows without an adapter
+        const uint16_t* from = (const uint16_t*)args.base + (row0 + col) * args.ldb;
+        uint16_t* to = (uint16_t*)args.out + (row0 + col) * args.ldo;
+        for (int64_t n0 = first; n0 < end; n0 += kUpCols)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int64_t n = n0 + column(half, g);
+                if (n0 < whole) *(u32x4_any*)(to + n) = *(const u32x4_any*)(from + n);
+                else store_end(to, n, args.N, load_end(from, n, args.N));
+            }
+    }
     for (int turn = 0; todo; ++turn) {   // every turn clears a bit
-        const int adapter = __builtin_amdgcn_readlane(id, __ffsll(todo) - 1);
+        const int one_row = __ffsll(todo) - 1;
+        const int adapter = __builtin_amdgcn_readlane(id, one_row);
         const unsigned long long same = __ballot(id == adapter);
         todo &= ~same;
         if (turn % args.up_z != (int)blockIdx.z) continue;
 
-        const float scale = args.scale ? args.scale[adapter] : 1.0f;
-        u32x4 high[RT][KH], low[RT][KH];
-        float back[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int64_t row = min(row0 + rt * 16 + col, args.M - 1);
-            float v[KH][8], most = 0.0f;
-#pragma unroll
-            for (int kh = 0; kh < KH; ++kh) {
-                const int rank = (kh * 4 + g) * 8;
-                f32x4 p = {}, q = {};
-                if (rank < args.R) {
-                    const float* h = args.h + row * args.R + rank;
-                    for (int s = 0; s < args.splits; ++s) {
-                        p += *(const f32x4*)h;
-                        q += *(const f32x4*)(h + 4);
-                        h += args.M * args.R;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[kh][i] = (i < 4 ? p[i] : q[i - 4]) * scale;
-                    most = fmaxf(most, fabsf(v[kh][i]));
-                }
-            }
-            back[rt] = 1.0f;
-            if constexpr (!BF16) {
-                // by a power of two to below 2^14, where neither part leaves fp16's range
-                most = fmaxf(most, __shfl_xor(most, 16, 64));
-                most = fmaxf(most, __shfl_xor(most, 32, 64));
-                const int e = (int)(__float_as_uint(most) >> 23) - 127;   // 128: not finite
-                const int shift = e == 128 ? 0 : min(13 - e, 120);
-                const float by = __uint_as_float((uint32_t)(127 + shift) << 23);
-                back[rt] = __uint_as_float((uint32_t)(127 - shift) << 23);
-#pragma unroll
-                for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[kh][i] *= by;
-            }
-#pragma unroll
-            for (int kh = 0; kh < KH; ++kh) split8(v[kh], high[rt][kh], low[rt][kh]);
-        }
+        // columns of the matrix instruction that are not the adapter's rows read what one
+        // of its rows reads, so that no load has a condition
+        const bool mine = same >> col & 1;
+        const int64_t row = row0 + (mine ? col : one_row);
+        const uint16_t* base = (const uint16_t*)args.base + row * args.ldb;
+        uint16_t* out = (uint16_t*)args.out + row * args.ldo;
         const uint16_t* b = (const uint16_t*)args.b + (int64_t)adapter * args.N * args.R;
-        for (int64_t n0 = run0 * kUpCols; n0 < n_end; n0 += kUpCols) {
-            u32x4 w[4][KH];
+        u32x4 w[4][KH], y[kRing][2];
+        if (first < whole) load_adapter<KH, true>(w, b, first, args.N, args.R, col, g);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t n = min(n0 + col / 4 * 16 + t * 4 + col % 4, args.N - 1);
+        for (int j = 0; j < kRing; ++j)
+            if (first + j * kUpCols < whole)
+                load_base<true>(y[j], base, first + j * kUpCols, args.N, g);
+
+        u32x4 high[KH], low[KH];
+        const float back = make_operands<KH>(high, low, args, row, adapter, g);
+
+        f32x4 d[4];
+        int64_t n0 = first;
+        while (n0 < whole) {
 #pragma unroll
-                for (int kh = 0; kh < KH; ++kh) {
-                    const int rank = (kh * 4 + g) * 8;
-                    w[t][kh] = u32x4{0u, 0u, 0u, 0u};
-                    if (rank < args.R) w[t][kh] = *(const u32x4*)(b + n * args.R + rank);
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                f32x4 d[4] = {};
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int kh = 0; kh < KH; ++kh) {
-                        d[t] = mfma(w[t][kh], high[rt][kh], d[t]);
-                        d[t] = mfma(w[t][kh], low[rt][kh], d[t]);
-                    }
-                if (same >> (rt * 16 + col) & 1) {
-                    const int64_t row = row0 + rt * 16 + col;
-                    const uint16_t* from = (const uint16_t*)args.base + row * args.ldb;
-                    uint16_t* to = (uint16_t*)args.out + row * args.ldo;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = d[half * 2 + i / 4][i % 4] * back[rt];
-                        const int64_t n = n0 + g * 16 + half * 8;
-                        if (n < args.N) add8(from, to, n, args.N, v);
-                    }
-                }
+            for (int j = 0; j < kRing; ++j) {
+                multiply<KH>(d, w, high, low, args.R, g);
+                if (n0 + kUpCols < whole)
+                    load_adapter<KH, true>(w, b, n0 + kUpCols, args.N, args.R, col, g);
+                add_run<true>(d, y[j], back, out, mine, n0, args.N, g);
+                if (n0 + kRing * kUpCols < whole)
+                    load_base<true>(y[j], base, n0 + kRing * kUpCols, args.N, g);
+                n0 += kUpCols;
+                if (n0 >= whole) break;
             }
         }
+        if (n0 < end) {   // N ends inside this run
+            load_adapter<KH, false>(w, b, n0, args.N, args.R, col, g);
+            load_base<false>(y[0], base, n0, args.N, g);
+            multiply<KH>(d, w, high, low, args.R, g);
+            add_run<false>(d, y[0], back, out, mine, n0, args.N, g);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows.  A load whose lanes stand in 16 rows, as the matrix instruction wants them, runs
+// at a quarter of the rate of one whose neighbouring lanes read neighbouring bytes, and
+// with many rows that rate is what counts: here x and the adapter are read in whole pieces
+// of rows and reach the matrix instruction through LDS, the adapter once for 64 rows.
+// ---------------------------------------------------------------------------
+
+constexpr int kPitch = kStep * 2 + 16;   // bytes of a row in LDS: 16 lanes touch 64 banks
+
+constexpr int kWideAhead = 2;   // pairs of steps in flight
+
+// First product: waves are 4 tiles of 16 rows by the 2 halves of a pair of steps.
+template <bool FP8, int RG>
+__global__ __launch_bounds__(512, 2) void down_wide_kernel(LoraArgs args) {
+    __shared__ __attribute__((aligned(16))) uint8_t ranks[2][2][RG * 16 * kPitch];
+    __shared__ __attribute__((aligned(16))) uint8_t rows[8][16 * kPitch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = wave & 3, half = wave >> 2, thread = threadIdx.x & 255;
+    const int col = lane & 15, g = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * 64;
+    const int slices = (args.R + 16 * RG - 1) / (16 * RG);
+    const int split = blockIdx.y / slices, rank0 = blockIdx.y % slices * (16 * RG);
+    const int steps = (int)((args.K + kStep - 1) / kStep);
+    const int from = (int)((int64_t)steps * split / args.splits);
+    const int to = (int)((int64_t)steps * (split + 1) / args.splits);
+    const int turns = (to - from + 1) / 2;
+
+    const int id = row_id(args, row0, 64, lane);
+    unsigned long long todo = __ballot(id >= 0);
+
+    // x: a load takes pieces of 16 bytes of 4 rows (E4M3: 8), side by side
+    constexpr int kLoads = FP8 ? 2 : 4, kPieces = FP8 ? 8 : 16;
+    constexpr int kBytes = FP8 ? 1 : 2;
+    const uint8_t* x[kLoads];
+    const int x_at = lane % kPieces * (16 / kBytes);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int64_t row = min(row0 + tile * 16 + i * (64 / kPieces) + lane / kPieces, args.M - 1);
+        x[i] = (const uint8_t*)args.x + (row * args.ldx + x_at) * kBytes;
+    }
+    const float* xs = FP8 ? args.xs + min(row0 + tile * 16 + col, args.M - 1) * args.KB : nullptr;
+    uint8_t* my_rows = rows[wave];
+    const u32x4 zeros = {0u, 0u, 0u, 0u};
+
+    while (todo) {   // every turn clears a bit
+        const int adapter = __builtin_amdgcn_readlane(id, __ffsll(todo) - 1);
+        const unsigned long long same = __ballot(id == adapter);
+        todo &= ~same;
+        const bool wanted = same >> (tile * 16) & 0xFFFFu;   // the same for the wave
+
+        const uint16_t* a[RG];
+        const int a_at = thread % 16 * 8;
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) {
+            const int rank = min(rank0 + rg * 16 + thread / 16, args.R - 1);
+            a[rg] = (const uint16_t*)args.a + ((int64_t)adapter * args.R + rank) * args.K + a_at;
+        }
+        // loads return in order: what is needed first is issued first, both as far ahead
+        u32x4 xr[kWideAhead][kLoads], ar[kWideAhead][RG];
+        float sr[kWideAhead];
+        auto load_x = [&](u32x4 (&r)[kLoads], float& s, int step) {
+            if (step >= to || !wanted) return;
+            const int64_t k = (int64_t)step * kStep;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                r[i] = zeros;
+                if (k + kStep <= args.K || k + x_at < args.K)
+                    r[i] = __builtin_nontemporal_load((const u32x4*)(x[i] + k * kBytes));
+            }
+            if constexpr (FP8) s = xs[step];
+        };
+        auto load_a = [&](u32x4 (&r)[RG], int step) {
+            if (step >= to) return;
+            const int64_t k = (int64_t)step * kStep;
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) {
+                r[rg] = zeros;
+                if (k + kStep <= args.K || k + a_at < args.K) r[rg] = *(const u32x4*)(a[rg] + k);
+            }
+        };
+        f32x4 acc[RG] = {};
+        int step = from + half;
+#pragma unroll
+        for (int j = 0; j < kWideAhead; ++j) {
+            load_a(ar[j], step + 2 * j);
+            load_x(xr[j], sr[j], step + 2 * j);
+        }
+        for (int turn = 0; turn < turns;) {
+#pragma unroll
+            for (int j = 0; j < kWideAhead; ++j) {
+                uint8_t* my_ranks = ranks[j & 1][half];
+#pragma unroll
+                for (int rg = 0; rg < RG; ++rg)
+                    *(u32x4*)(my_ranks + (rg * 16 + thread / 16) * kPitch + a_at * 2) = ar[j][rg];
+                const bool here = wanted && step < to;
+                float scale = 1.0f;
+                if (here) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        uint8_t* to_row = my_rows + (i * (64 / kPieces) + lane / kPieces) * kPitch +
+                                          x_at * 2;
+                        const u32x4 q = xr[j][i];
+                        if constexpr (FP8) {
+                            *(u32x4*)to_row = u32x4{widen<false>(q[0]), widen<true>(q[0]),
+                                                    widen<false>(q[1]), widen<true>(q[1])};
+                            *(u32x4*)(to_row + 16) = u32x4{widen<false>(q[2]), widen<true>(q[2]),
+                                                           widen<false>(q[3]), widen<true>(q[3])};
+                        } else {
+                            *(u32x4*)to_row = q;
+                        }
+                    }
+                    if constexpr (FP8) scale = sr[j];
+                }
+                load_a(ar[j], step + 2 * kWideAhead);
+                load_x(xr[j], sr[j], step + 2 * kWideAhead);
+                __syncthreads();
+                if (here) {
+                    f32x4 c[RG];
+#pragma unroll
+                    for (int rg = 0; rg < RG; ++rg)
+                        c[rg] = FP8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[rg];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const u32x4 b = *(const u32x4*)(my_rows + col * kPitch + (i * 4 + g) * 16);
+#pragma unroll
+                        for (int rg = 0; rg < RG; ++rg)
+                            c[rg] = mfma(*(const u32x4*)(my_ranks + (rg * 16 + col) * kPitch +
+                                                         (i * 4 + g) * 16),
+                                         b, c[rg]);
+                    }
+#pragma unroll
+                    for (int rg = 0; rg < RG; ++rg) {
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[rg][i] = __builtin_fmaf(c[rg][i], scale, acc[rg][i]);
+                        } else {
+                            acc[rg] = c[rg];
+                        }
+                    }
+                }
+                step += 2;
+                if (++turn >= turns) break;   // the same for the workgroup
+            }
+        }
+        // the two halves' sums; a lane's numbers are 4 consecutive ranks of one row
+        __syncthreads();
+        f32x4* other = (f32x4*)ranks[0][0] + tile * RG * 64;
+        if (half == 1)
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) other[rg * 64 + lane] = acc[rg];
+        __syncthreads();
+        if (half == 0 && (same >> (tile * 16 + col) & 1))
+#pragma unroll
+            for (int rg = 0; rg < RG; ++rg) {
+                const int rank = rank0 + rg * 16 + g * 4;
+                const int64_t row = (int64_t)split * args.M + row0 + tile * 16 + col;
+                if (rank < args.R)
+                    *(f32x4*)(args.h + row * args.R + rank) = acc[rg] + other[rg * 64 + lane];
+            }
+        __syncthreads();
+    }
+}
+
+constexpr int kWideCols = 128;   // columns of a run
+constexpr int kWideRing = 2;     // runs of base in flight
+
+// Second product: waves are 4 tiles of 16 rows; a run of columns of the adapter goes
+// through LDS.  h is the first operand, so a lane ends with rows g * 4 + j; the columns are
+// dealt (column 8 i + t is number i of operand t) so that it has 8 consecutive ones of
+// each, and 16 lanes 256 bytes of a row.
+template <int KH>
+__global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs args) {
+    constexpr int kRowPitch = KH * 64 + 16;   // as kPitch
+    constexpr int kLoads = KH * 2;            // 16-byte pieces of a run per thread, at most
+    __shared__ __attribute__((aligned(16))) uint8_t ranks[2][kWideCols * kRowPitch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    // a block of columns stays on one XCD (workgroups are dealt over the 8 of them), so that
+    // its numbers of the adapter are in one L2
+    const int64_t blocks = (args.N + args.up_each * kWideCols - 1) / (args.up_each * kWideCols);
+    const uint32_t deal = blockIdx.x / 8, per_xcd = ((uint32_t)blocks + 7) / 8;
+    const int64_t block = deal % per_xcd * 8 + blockIdx.x % 8;
+    if (block >= blocks) return;
+    const int64_t row0 = (int64_t)(deal / per_xcd) * 64;
+    const int64_t tile0 = row0 + wave * 16;
+    const int64_t first = block * args.up_each * kWideCols;
+    const int64_t end = min(args.N, first + (int64_t)args.up_each * kWideCols);
+    const int64_t whole = min(end, args.N / kWideCols * kWideCols);
+    const int64_t mine0 = first + col * 8;   // the lane's first column
+
+    const int id = row_id(args, row0, 64, lane);
+    unsigned long long todo = __ballot(id >= 0);
+    if (args.out != args.base) {   // rows without an adapter
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = wave * 16 + g * 4 + j;
+            if ((todo >> r & 1) || row0 + r >= args.M) continue;
+            const uint16_t* from = (const uint16_t*)args.base + (row0 + r) * args.ldb;
+            uint16_t* to = (uint16_t*)args.out + (row0 + r) * args.ldo;
+            for (int64_t n = mine0; n < end + col * 8; n += kWideCols) {
+                if (n - col * 8 < whole) *(u32x4_any*)(to + n) = *(const u32x4_any*)(from + n);
+                else store_end(to, n, args.N, load_end(from, n, args.N));
+            }
+        }
+    }
+    if (todo == 0) return;
+
+    // Where the pieces of a run go: piece q is 8 ranks of column q / (R / 8); pieces of
+    // ranks behind R stay zeros.
+    const int per_col = args.R / 8, pieces = kWideCols * per_col;
+    int place[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int q = threadIdx.x + i * 256, n = q / per_col;
+        place[i] = (n % 8 * 16 + n / 8) * kRowPitch + q % per_col * 16;
+    }
+    if (args.R % 32) {
+        for (int n = threadIdx.x; n < 2 * kWideCols; n += 256)
+            for (int c = per_col; c < KH * 4; ++c)
+                *(u32x4*)(ranks[n / kWideCols] + n % kWideCols * kRowPitch + c * 16) =
+                    u32x4{0u, 0u, 0u, 0u};
+    }
+    while (todo) {   // every turn clears a bit
+        const int adapter = __builtin_amdgcn_readlane(id, __ffsll(todo) - 1);
+        const unsigned long long same = __ballot(id == adapter);
+        todo &= ~same;
+        const uint32_t tile_rows = (uint32_t)(same >> (wave * 16)) & 0xFFFFu;
+        const bool wanted = tile_rows != 0;   // the same for the wave
+        const int one_row = wanted ? __builtin_ctz(tile_rows) : 0;
+
+        const uint16_t* b = (const uint16_t*)args.b + (int64_t)adapter * args.N * args.R;
+        u32x4 w[kLoads], y[kWideRing][4];
+        auto load_adapter = [&](int64_t n0) {
+            const uint8_t* run = (const uint8_t*)(b + n0 * args.R);
+            const int64_t left = (args.N - n0) * per_col;   // pieces of the columns inside N
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int q = threadIdx.x + i * 256;
+                if (q < pieces && q < left) w[i] = *(const u32x4*)(run + q * 16);
+            }
+        };
+        const uint16_t* base[4];
+        uint16_t* out[4];
+        const bool mine[4] = {(tile_rows >> (g * 4) & 1) != 0, (tile_rows >> (g * 4 + 1) & 1) != 0,
+                              (tile_rows >> (g * 4 + 2) & 1) != 0,
+                              (tile_rows >> (g * 4 + 3) & 1) != 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // other rows read what one of the adapter's reads
+            const int64_t row = tile0 + (mine[j] ? g * 4 + j : one_row);
+            base[j] = (const uint16_t*)args.base + row * args.ldb + mine0;
+            out[j] = (uint16_t*)args.out + row * args.ldo + mine0;
+        }
+        auto load_base_run = [&](u32x4 (&r)[4], int64_t n0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[j] = __builtin_nontemporal_load((const u32x4_any*)(base[j] + (n0 - first)));
+        };
+        load_adapter(first);
+        u32x4 high[KH], low[KH];
+        float back[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (wanted) {
+#pragma unroll
+            for (int j = 0; j < kWideRing; ++j)
+                if (first + j * kWideCols < whole)
+                    load_base_run(y[j], first + j * kWideCols);
+            const int64_t row = tile0 + (tile_rows >> col & 1 ? col : one_row);
+            const float by = make_operands<KH>(high, low, args, row, adapter, g);
+            if constexpr (!BF16)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) back[j] = __shfl(by, g * 4 + j, 64);
+        }
+        for (int64_t n0 = first; n0 < end;) {
+#pragma unroll
+            for (int j = 0; j < kWideRing; ++j) {
+                uint8_t* my_ranks = ranks[j & 1];
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    if ((int)threadIdx.x + i * 256 < pieces) *(u32x4*)(my_ranks + place[i]) = w[i];
+                if (n0 + kWideCols < end) load_adapter(n0 + kWideCols);
+                __syncthreads();
+                if (wanted) {
+                    f32x4 d[8] = {};
+#pragma unroll
+                    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            const u32x4 q = *(const u32x4*)(my_ranks + (t * 16 + col) * kRowPitch +
+                                                            (kh * 4 + g) * 16);
+                            d[t] = mfma(high[kh], q, d[t]);
+                            d[t] = mfma(low[kh], q, d[t]);
+                        }
+                    if (n0 < whole) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const f32x4 p = {d[0][r], d[1][r], d[2][r], d[3][r]};
+                            const f32x4 q = {d[4][r], d[5][r], d[6][r], d[7][r]};
+                            const u32x4 v = add8(y[j][r], p, q, back[r]);
+                            if (mine[r]) *(u32x4_any*)(out[r] + (n0 - first)) = v;
+                        }
+                        if (n0 + kWideRing * kWideCols < whole)
+                            load_base_run(y[j], n0 + kWideRing * kWideCols);
+                    } else {   // N ends inside this run
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const f32x4 p = {d[0][r], d[1][r], d[2][r], d[3][r]};
+                            const f32x4 q = {d[4][r], d[5][r], d[6][r], d[7][r]};
+                            const int64_t n = n0 + col * 8;
+                            if (mine[r])
+                                store_end(out[r] - mine0, n, args.N,
+                                          add8(load_end(base[r] - mine0, n, args.N), p, q, back[r]));
+                        }
+                    }
+                }
+                n0 += kWideCols;
+                if (n0 >= end) break;   // the same for the workgroup
+            }
+        }
+        __syncthreads();   // the next turn writes the first buffer again
     }
 }
 
 // ---- launches
 
-template <bool FP8, int RT, int RG>
+template <bool FP8, int RG>
 hipError_t down(const LoraArgs& a, hipStream_t stream) {
     const int slices = (a.R + 16 * RG - 1) / (16 * RG);
-    const dim3 grid((unsigned)((a.M + 16 * RT - 1) / (16 * RT)), (unsigned)(a.splits * slices),
-                    (unsigned)a.down_z);
-    down_kernel<FP8, RT, RG><<<grid, kDownWaves * 64, 0, stream>>>(a);
+    if (a.many) {
+        const dim3 grid((unsigned)((a.M + 63) / 64), (unsigned)(a.splits * slices));
+        down_wide_kernel<FP8, RG><<<grid, 512, 0, stream>>>(a);
+    } else {
+        const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)(a.splits * slices),
+                        (unsigned)a.down_z);
+        down_kernel<FP8, RG><<<grid, kDownWaves * 64, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
 template <bool FP8>
 hipError_t down_any(const LoraArgs& a, hipStream_t stream) {
-    const bool many = a.down_tiles > 1;
-    if (a.R <= 16) return many ? down<FP8, 4, 1>(a, stream) : down<FP8, 1, 1>(a, stream);
-    if (a.R <= 32) return many ? down<FP8, 4, 2>(a, stream) : down<FP8, 1, 2>(a, stream);
-    return many ? down<FP8, 2, 4>(a, stream) : down<FP8, 1, 4>(a, stream);
+    switch (rank_groups(a.R)) {
+        case 1: return down<FP8, 1>(a, stream);
+        case 2: return down<FP8, 2>(a, stream);
+        case 3: return down<FP8, 3>(a, stream);
+        default: return down<FP8, 4>(a, stream);
+    }
 }
 
-template <int RT, int KH>
+template <int KH>
 hipError_t up(const LoraArgs& a, hipStream_t stream) {
-    const int64_t cols = (int64_t)kUpCols * kUpWaves * a.up_each;
-    const dim3 grid((unsigned)((a.M + 16 * RT - 1) / (16 * RT)), (unsigned)((a.N + cols - 1) / cols),
-                    (unsigned)a.up_z);
-    up_kernel<RT, KH><<<grid, kUpWaves * 64, 0, stream>>>(a);
+    if (a.many) {
+        const int64_t cols = (int64_t)kWideCols * a.up_each;
+        const int64_t blocks = (a.N + cols - 1) / cols;
+        up_wide_kernel<KH><<<(unsigned)((a.M + 63) / 64 * ((blocks + 7) / 8 * 8)), 256, 0, stream>>>(a);
+    } else {
+        const int64_t cols = (int64_t)kUpCols * (kUpWaves / a.up_wide) * a.up_each;
+        const dim3 grid((unsigned)((a.M + 16 * a.up_wide - 1) / (16 * a.up_wide)),
+                        (unsigned)((a.N + cols - 1) / cols), (unsigned)a.up_z);
+        up_kernel<KH><<<grid, kUpWaves * 64, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
 hipError_t up_any(const LoraArgs& a, hipStream_t stream) {
-    const bool many = a.up_tiles > 1;
-    if (a.R <= 32) return many ? up<4, 1>(a, stream) : up<1, 1>(a, stream);
-    if (a.R <= 64) return many ? up<4, 2>(a, stream) : up<1, 2>(a, stream);
-    if (a.R <= 128) return many ? up<2, 4>(a, stream) : up<1, 4>(a, stream);
-    return up<1, 8>(a, stream);
+    switch ((a.R + 31) / 32) {   // all but the last operand are whole: loads stay inside rows of b
+        case 1: return up<1>(a, stream);
+        case 2: return up<2>(a, stream);
+        case 3: return up<3>(a, stream);
+        case 4: return up<4>(a, stream);
+        case 5: return up<5>(a, stream);
+        case 6: return up<6>(a, stream);
+        case 7: return up<7>(a, stream);
+        default: return up<8>(a, stream);
+    }
 }
 
 hipError_t both(const LoraArgs& a, bool x_fp8, hipStream_t stream) {

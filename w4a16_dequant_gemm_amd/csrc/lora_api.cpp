@@ -39,22 +39,28 @@ bool stride_ok(int64_t ld, int64_t W, int64_t M) {
 // ids, and the workspace is known before the call.
 void set_plan(LoraArgs& a) {
     const int steps = (int)ceil_div(a.K, kStep);
-    // first product: row tiles share the loads of A once there are workgroups enough
-    a.down_tiles = a.M >= 1024 ? (a.R <= 32 ? 4 : 2) : 1;
-    const int64_t groups = ceil_div(a.M, 16 * a.down_tiles);
-    const int64_t slices = ceil_div(a.R, a.R <= 16 ? 16 : a.R <= 32 ? 32 : 64);
-    a.splits = (int32_t)std::min<int64_t>({std::max<int64_t>(1, 512 / (groups * slices)),
-                                           ceil_div(steps, kDownWaves), 16});
-    const int64_t most = std::min<int64_t>(16 * a.down_tiles, std::min<int64_t>(a.L, a.M));
-    a.down_z = (int32_t)std::clamp<int64_t>(1024 / (groups * slices * a.splits), 1, most);
+    a.many = a.M >= 512;
+    // first product: K in parts until there is a workgroup for every CU
+    const int64_t groups = ceil_div(a.M, a.many ? 64 : 16) * rank_slices(a.R);
+    a.splits = (int32_t)std::clamp<int64_t>(
+        256 / groups, 1, std::min<int64_t>(ceil_div(steps, a.many ? 4 : kDownWaves), 16));
+    const int64_t most = std::min<int64_t>(16, std::min<int64_t>(a.L, a.M));
+    a.down_z = (int32_t)std::clamp<int64_t>(512 / (groups * a.splits), 1, most);
     // second product
-    a.up_tiles = a.M < 512 ? 1 : a.R <= 64 ? 4 : a.R <= 128 ? 2 : 1;
-    const int64_t rows = ceil_div(a.M, 16 * a.up_tiles), runs = ceil_div(a.N, kUpCols);
-    a.up_each = (int32_t)std::clamp<int64_t>(rows * runs / 8192, 1, 4);
-    if (a.N >= (int64_t)1 << 23) a.up_each = 4;   // the grid's second dimension stays below 2^16
-    const int64_t waves = rows * ceil_div(runs, a.up_each);
-    a.up_z = (int32_t)std::clamp<int64_t>(
-        32768 / waves, 1, std::min<int64_t>(16 * a.up_tiles, std::min<int64_t>(a.L, a.M)));
+    const int64_t runs = ceil_div(a.N, a.many ? 128 : kUpCols);
+    const int64_t tiles = ceil_div(a.M, a.many ? 64 : 16);
+    if (a.many) {
+        // two workgroups per CU, twice, in blocks of columns that the 8 XCDs share evenly
+        const int64_t blocks = std::clamp<int64_t>(1024 / tiles / 8 * 8, 8, runs);
+        a.up_each = (int32_t)ceil_div(runs, blocks);
+        a.up_z = a.up_wide = 1;
+        return;
+    }
+    a.up_wide = tiles >= 8 ? 4 : 1;
+    a.up_each = (int32_t)std::clamp<int64_t>(tiles * runs / 8192, 1, 16);
+    if (a.N >= (int64_t)1 << 23) a.up_each = 16;   // the grid's second dimension stays below 2^16
+    const int64_t waves = tiles * ceil_div(runs, a.up_each);
+    a.up_z = (int32_t)std::clamp<int64_t>(4096 / waves, 1, most);
 }
 
 size_t bytes_of(const LoraArgs& a) {

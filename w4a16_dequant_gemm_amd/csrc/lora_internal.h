@@ -12,7 +12,7 @@ namespace lora {
 constexpr int64_t kSkip = 65536;   // the workspace's first bytes hold the products' counters
 constexpr int kStep = 128;         // reduction indices of a wave's step; also of an fp8 scale
 constexpr int kDownWaves = 8;      // waves of a workgroup of the first product: they share K
-constexpr int kUpWaves = 4;        // of the second: each has columns of its own
+constexpr int kUpWaves = 4;        // of the second: each works for itself
 constexpr int kUpCols = 64;        // columns a wave of the second product makes at a time
 
 struct LoraArgs {
@@ -27,12 +27,17 @@ struct LoraArgs {
     float* h;             // [splits][M][R]: partial inner products with A
     int64_t ldb, ldx, ldo, M, N, K;
     int32_t R, L, KB;     // KB: fp8 scales per row
+    int32_t many;         // the forms for many rows
     int32_t splits;       // parts of K over workgroups
-    int32_t down_tiles;   // tiles of 16 rows per workgroup of the first product
     int32_t down_z;       // workgroups that share a row group's adapters
-    int32_t up_tiles, up_z;
+    int32_t up_wide;      // waves of a workgroup of the second product side by side in rows: 4 or 1
+    int32_t up_z;
     int32_t up_each;      // runs of kUpCols columns per wave
 };
+
+// Ranks in workgroups of the first product: slices of at most 64, groups of 16 in each.
+inline int rank_slices(int R) { return (R + 63) / 64; }
+inline int rank_groups(int R) { return ((R + 15) / 16 + rank_slices(R) - 1) / rank_slices(R); }
 
 hipError_t launch_f16(const LoraArgs& a, bool x_fp8, hipStream_t stream);
 hipError_t launch_bf16(const LoraArgs& a, bool x_fp8, hipStream_t stream);

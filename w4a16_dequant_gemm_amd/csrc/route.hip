@@ -439,44 +439,83 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
 // once; the runs' sums are added in their order.
 constexpr int kScanCols = 16, kScanRuns = 64, kScanEach = 16;
 
+// Sums over the runs of the tiles that this and all threads of a column hold: a run is a
+// group of 16 lanes, 4 of them in a wave.
+struct RunSums {
+    int before, all;
+};
+
+__device__ __forceinline__ RunSums sum_runs(int mine, int (*part)[kScanCols]) {
+    const int c = threadIdx.x % kScanCols, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int upto = mine;
+    int other = __shfl_up(upto, 16, 64);
+    if (lane >= 16) upto += other;
+    other = __shfl_up(upto, 32, 64);
+    if (lane >= 32) upto += other;
+    if (lane >= 48) part[wave][c] = upto;
+    __syncthreads();
+    RunSums sum = {upto - mine, 0};
+#pragma unroll
+    for (int w = 0; w < kScanRuns / 4; ++w) {
+        const int p = part[w][c];
+        if (w < wave) sum.before += p;
+        sum.all += p;
+    }
+    __syncthreads();
+    return sum;
+}
+
+// The same runs' floats, in their order; the result is for the threads of wave 0.
+__device__ __forceinline__ float sum_runs(float mine, float (*part)[kScanCols]) {
+    const int c = threadIdx.x % kScanCols, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    mine += __shfl_down(mine, 16, 64);
+    mine += __shfl_down(mine, 32, 64);
+    if (lane < 16) part[wave][c] = mine;
+    __syncthreads();
+    float sum = 0.0f;
+    if (wave == 0)
+#pragma unroll
+        for (int w = 0; w < kScanRuns / 4; ++w) sum += part[w][c];
+    __syncthreads();
+    return sum;
+}
+
 template <bool LOSS>
 __global__ __launch_bounds__(kScanCols* kScanRuns) void sum_tiles_kernel(RouteArgs a) {
-    __shared__ int run_count[kScanRuns][kScanCols + 1];
-    __shared__ float run_p[kScanRuns][kScanCols + 1];
+    __shared__ int part[kScanRuns / 4][kScanCols];
+    __shared__ float part_p[kScanRuns / 4][kScanCols];
     const int c = threadIdx.x % kScanCols, run = threadIdx.x / kScanCols;
     const int e = blockIdx.x * kScanCols + c, E = a.E;
     int carry = 0;
     float all_p = 0.0f;
-    for (int64_t from = 0; from < a.tiles; from += kScanRuns * kScanEach) {
-        int n[kScanEach], mine = 0;
-        float p = 0.0f;
-        const int64_t b0 = from + run * kScanEach;
+    for (int from = 0; from < a.tiles; from += kScanRuns * kScanEach) {
+        // runs as long as what is left makes them
+        const int left = min(a.tiles - from, kScanRuns * kScanEach);
+        const int each = (left + kScanRuns - 1) / kScanRuns;
+        const int b0 = from + run * each, n = e <= E ? min(each, from + left - b0) : 0;
+        int32_t* at = a.tile_counts + (int64_t)b0 * (E + 1) + e;
+        int count[kScanEach], mine = 0;
 #pragma unroll
-        for (int i = 0; i < kScanEach; ++i)
-            n[i] = e <= E && b0 + i < a.tiles ? a.tile_counts[(b0 + i) * (E + 1) + e] : 0;
+        for (int i = 0; i < kScanEach; ++i) count[i] = i < n ? at[(int64_t)i * (E + 1)] : 0;
         if constexpr (LOSS) {
+            float p[kScanEach], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kScanEach; ++i)
-                p += e < E && b0 + i < a.tiles ? a.tile_p[(b0 + i) * E + e] : 0.0f;
+                p[i] = i < n && e < E ? a.tile_p[(int64_t)(b0 + i) * E + e] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kScanEach; ++i) sum += p[i];
+            all_p += sum_runs(sum, part_p);
         }
 #pragma unroll
-        for (int i = 0; i < kScanEach; ++i) mine += n[i];
-        run_count[run][c] = mine;
-        run_p[run][c] = p;
-        __syncthreads();
-        int before = carry;
-        for (int r = 0; r < kScanRuns; ++r) {
-            if (r < run) before += run_count[r][c];
-            carry += run_count[r][c];
-        }
-        if (LOSS && run == 0)
-            for (int r = 0; r < kScanRuns; ++r) all_p += run_p[r][c];
+        for (int i = 0; i < kScanEach; ++i) mine += count[i];
+        const RunSums sum = sum_runs(mine, part);
+        int before = carry + sum.before;
 #pragma unroll
         for (int i = 0; i < kScanEach; ++i) {
-            if (e < E && b0 + i < a.tiles) a.tile_counts[(b0 + i) * (E + 1) + e] = before;
-            before += n[i];
+            if (i < n && e < E) at[(int64_t)i * (E + 1)] = before;
+            before += count[i];
         }
-        __syncthreads();
+        carry += sum.all;
     }
     if (run == 0 && e <= E) {
         a.all_counts[e] = carry;
