@@ -5,8 +5,10 @@
 // Rows are taken 16 at a time as columns of the matrix instruction (v_mfma_f32_16x16x32,
 // the adapter is its first operand), so a row's result depends on that row and on
 // its own adapter only.  A row group that holds several adapters is done once for each,
-// and only that adapter's rows are stored: nothing is sorted, and no workgroup waits for
-// another.  The distinct adapters of a group are found with ballots over its ids.
+// and only that adapter's rows are stored.  The distinct adapters of a group are found with
+// ballots over its ids.  From 128 rows on the rows are first ordered by adapter, so that
+// there are few of them in a group (512 rows of 64 adapters at random, K = 8192, N = 28672,
+// R = 16: 251 -> ORDERED_US us); the order changes no result.
 //
 // Compiled once per activation dtype (LORA_TU_BF16 = 0 fp16, 1 bf16).
 #include <hip/hip_runtime.h>
@@ -23,6 +25,7 @@ namespace {
 
 constexpr bool BF16 = LORA_TU_BF16 != 0;
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -59,11 +62,83 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
                                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
 }
 
+// Rows are counted in the order of the calls' `order`, or as they are.
+__device__ __forceinline__ int64_t row_of(const LoraArgs& a, int64_t at) {
+    at = min(at, a.M - 1);
+    return a.order ? a.order[at] : at;
+}
+
 // The adapter of row `lane` of a group of `rows` rows from row0, -1 without one.
 __device__ __forceinline__ int row_id(const LoraArgs& a, int64_t row0, int rows, int lane) {
     int id = -1;
-    if (lane < rows && row0 + lane < a.M) id = a.ids[row0 + lane];
+    if (lane < rows && row0 + lane < a.M) id = a.order ? a.sorted[row0 + lane] : a.ids[row0 + lane];
     return id >= 0 && id < a.L ? id : -1;
+}
+
+// Rows by adapter, those without one last: a counting sort over the ids' remainders (a
+// group of rows may hold anything, so adapters that share a remainder only cost time).  One
+// workgroup: 4096 rows take SORT_US us.
+constexpr int kBins = 1024;
+
+// Adds one for every live lane to its bin; returns what the lane found there.  Lanes of one
+// bin (runs of a request) take one addition.
+__device__ __forceinline__ int count_up(int* bins, int bin, bool live) {
+    const unsigned long long lanes = __ballot(live);
+    if (lanes == 0) return 0;
+    const int one = __builtin_amdgcn_readlane(bin, __ffsll(lanes) - 1);
+    if (__ballot(live && bin == one) != lanes) return live ? atomicAdd(&bins[bin], 1) : 0;
+    const int lane = threadIdx.x & 63;
+    const int below = __popcll(lanes & ((1ull << lane) - 1));
+    int first = 0;
+    if (live && below == 0) first = atomicAdd(&bins[one], __popcll(lanes));
+    return __builtin_amdgcn_readlane(first, __ffsll(lanes) - 1) + below;
+}
+
+__global__ __launch_bounds__(1024) void sort_kernel(LoraArgs args) {
+    constexpr int kKept = 8;   // ids per thread in registers: more are read again
+    __shared__ int first[kBins];
+    __shared__ int part[16];
+    const int t = threadIdx.x;
+    auto bin = [&](int id) { return id >= 0 && id < args.L ? id % (kBins - 1) : kBins - 1; };
+    int kept[kKept];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        kept[i] = t + i * 1024 < args.M ? args.ids[t + i * 1024] : -1;
+    first[t] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (i * 1024 < args.M) count_up(first, bin(kept[i]), t + i * 1024 < args.M);
+    for (int64_t from = kKept * 1024; from < args.M; from += 1024) {
+        const int64_t row = from + t;
+        count_up(first, bin(row < args.M ? args.ids[row] : -1), row < args.M);
+    }
+    __syncthreads();
+    const int mine = first[t];
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int other = __shfl_up(upto, off, 64);
+        if ((t & 63) >= off) upto += other;
+    }
+    if ((t & 63) == 63) part[t >> 6] = upto;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < (t >> 6); ++w) before += part[w];
+    first[t] = before + upto - mine;
+    __syncthreads();
+    auto put = [&](int64_t row, int id) {
+        const int at = count_up(first, bin(id), row < args.M);
+        if (row < args.M) {
+            args.order[at] = (int)row;
+            args.sorted[at] = id;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (i * 1024 < args.M) put(t + i * 1024, kept[i]);
+    for (int64_t from = kKept * 1024; from < args.M; from += 1024)
+        put(from + t, from + t < args.M ? args.ids[from + t] : -1);
 }
 
 // ---------------------------------------------------------------------------
@@ -161,7 +236,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
     unsigned long long todo = __ballot(id >= 0);
     if (todo == 0) return;
 
-    const int64_t row = min(row0 + col, args.M - 1);
+    const int64_t row = row_of(args, row0 + col);
     const uint8_t* x = (const uint8_t*)args.x + row * args.ldx * (FP8 ? 1 : 2);
     const float* xs = FP8 ? args.xs + row * args.KB : nullptr;
     for (int turn = 0; todo; ++turn) {   // every turn clears a bit
@@ -227,21 +302,31 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
-// 8 numbers as two operands whose sum they are (to 16 bits bf16, 22 bits fp16); what is
-// not finite stands in the high one alone.
+// A number as two 16-bit ones whose sum it is (to 17 bits bf16, 22 bits fp16); what is not
+// finite stands in the high one alone.
+__device__ __forceinline__ void split(float v, uint32_t& high, uint32_t& low) {
+    high = to_half(v);
+    low = finite(v) ? to_half(v - to_float(high)) : 0u;
+}
+
 __device__ __forceinline__ void split8(const float (&v)[8], u32x4& high, u32x4& low) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float x = v[2 * i + k];
-            hi[k] = to_half(x);
-            lo[k] = finite(x) ? to_half(x - to_float(hi[k])) : 0u;
-        }
-        high[i] = hi[0] | hi[1] << 16;
-        low[i] = lo[0] | lo[1] << 16;
+        uint32_t h0, l0, h1, l1;
+        split(v[2 * i], h0, l0);
+        split(v[2 * i + 1], h1, l1);
+        high[i] = h0 | h1 << 16;
+        low[i] = l0 | l1 << 16;
     }
+}
+
+// The power of two that brings fp16's rows, whose largest number is `most`, to below 2^14,
+// where neither part leaves the type's range; back: its reciprocal.
+[[maybe_unused]] __device__ __forceinline__ float power_for(float most, float& back) {
+    const int e = (int)(__float_as_uint(most) >> 23) - 127;   // 128: not finite
+    const int shift = e == 128 ? 0 : min(13 - e, 120);
+    back = __uint_as_float((uint32_t)(127 - shift) << 23);
+    return __uint_as_float((uint32_t)(127 + shift) << 23);
 }
 
 // A row's h (lane group g: every fourth run of 8 ranks) into operands, splits of a number
@@ -283,14 +368,9 @@ __device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[K
     }
     float back = 1.0f;
     if constexpr (!BF16) {
-        // a row's numbers by a power of two to below 2^14, where neither part leaves
-        // fp16's range
         most = fmaxf(most, __shfl_xor(most, 16, 64));
         most = fmaxf(most, __shfl_xor(most, 32, 64));
-        const int e = (int)(__float_as_uint(most) >> 23) - 127;   // 128: not finite
-        const int shift = e == 128 ? 0 : min(13 - e, 120);
-        const float by = __uint_as_float((uint32_t)(127 + shift) << 23);
-        back = __uint_as_float((uint32_t)(127 - shift) << 23);
+        const float by = power_for(most, back);
 #pragma unroll
         for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
@@ -406,11 +486,12 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
     if (row0 >= args.M || first >= end) return;
 
     const int id = row_id(args, row0, 16, lane);
+    const int own = (int)row_of(args, row0 + col);
     unsigned long long todo = __ballot(id >= 0);
     if (blockIdx.z == 0 && args.out != args.base && !(todo >> col & 1) && row0 + col < args.M) {
         // rows without an adapter
-        const uint16_t* from = (const uint16_t*)args.base + (row0 + col) * args.ldb;
-        uint16_t* to = (uint16_t*)args.out + (row0 + col) * args.ldo;
+        const uint16_t* from = (const uint16_t*)args.base + own * args.ldb;
+        uint16_t* to = (uint16_t*)args.out + own * args.ldo;
         for (int64_t n0 = first; n0 < end; n0 += kUpCols)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -430,8 +511,9 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
         // of its rows reads, so that no load has a condition
         const bool mine = same >> col & 1;
         const int64_t row = row0 + (mine ? col : one_row);
-        const uint16_t* base = (const uint16_t*)args.base + row * args.ldb;
-        uint16_t* out = (uint16_t*)args.out + row * args.ldo;
+        const int64_t actual = mine ? own : __builtin_amdgcn_readlane(own, one_row);
+        const uint16_t* base = (const uint16_t*)args.base + actual * args.ldb;
+        uint16_t* out = (uint16_t*)args.out + actual * args.ldo;
         const uint16_t* b = (const uint16_t*)args.b + (int64_t)adapter * args.N * args.R;
         u32x4 w[4][KH], y[kRing][2];
         if (first < whole) load_adapter<KH, true>(w, b, first, args.N, args.R, col, g);
@@ -504,10 +586,10 @@ __global__ __launch_bounds__(512, 2) void down_wide_kernel(LoraArgs args) {
     const int x_at = lane % kPieces * (16 / kBytes);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int64_t row = min(row0 + tile * 16 + i * (64 / kPieces) + lane / kPieces, args.M - 1);
+        const int64_t row = row_of(args, row0 + tile * 16 + i * (64 / kPieces) + lane / kPieces);
         x[i] = (const uint8_t*)args.x + (row * args.ldx + x_at) * kBytes;
     }
-    const float* xs = FP8 ? args.xs + min(row0 + tile * 16 + col, args.M - 1) * args.KB : nullptr;
+    const float* xs = FP8 ? args.xs + row_of(args, row0 + tile * 16 + col) * args.KB : nullptr;
     uint8_t* my_rows = rows[wave];
     const u32x4 zeros = {0u, 0u, 0u, 0u};
 
@@ -631,6 +713,65 @@ __global__ __launch_bounds__(512, 2) void down_wide_kernel(LoraArgs args) {
     }
 }
 
+// The parts of h into the second product's operands: sums over the splits times the
+// adapter's scale, as high and low parts, ranks filled up to whole operands with zeros.
+// 16 lanes per row.  (Up to 500 rows every wave of the second product does this for itself:
+// there it costs less than a launch.)
+template <int KH>
+__global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
+    constexpr int kEach = (KH + 1) / 2;   // runs of 64 ranks, 4 per lane
+    const int lane = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+    if (row >= args.M) return;
+    const int id = args.order ? args.sorted[row] : args.ids[row];
+    if (id < 0 || id >= args.L) return;
+    const float scale = args.scale ? args.scale[id] : 1.0f;
+    f32x4 sum[kEach];
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int rank = i * 64 + lane * 4;
+        sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (rank < args.R) {
+            const float* h = args.h + row * args.R + rank;
+            int s = 0;
+            for (; s + 4 <= args.splits; s += 4) {
+                f32x4 p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    p[k] = *(const f32x4*)(h + (s + k) * args.M * args.R);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[i] += p[k];
+            }
+            for (; s < args.splits; ++s) sum[i] += *(const f32x4*)(h + s * args.M * args.R);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sum[i][k] *= scale;
+            most = fmaxf(most, fabsf(sum[i][k]));
+        }
+    }
+    float by = 1.0f;
+    if constexpr (!BF16) {
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+        float back;
+        by = power_for(most, back);
+        if (lane == 0) args.back[row] = back;
+    }
+    uint16_t* out = args.operands + row * (KH * 64);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int rank = i * 64 + lane * 4;
+        if (rank >= KH * 32) continue;
+        uint32_t high[4], low[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split(sum[i][k] * by, high[k], low[k]);
+        *(u32x2*)(out + rank) = u32x2{high[0] | high[1] << 16, high[2] | high[3] << 16};
+        *(u32x2*)(out + KH * 32 + rank) = u32x2{low[0] | low[1] << 16, low[2] | low[3] << 16};
+    }
+}
+
 constexpr int kWideCols = 128;   // columns of a run
 constexpr int kWideRing = 2;     // runs of base in flight
 
@@ -665,8 +806,9 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
         for (int j = 0; j < 4; ++j) {
             const int r = wave * 16 + g * 4 + j;
             if ((todo >> r & 1) || row0 + r >= args.M) continue;
-            const uint16_t* from = (const uint16_t*)args.base + (row0 + r) * args.ldb;
-            uint16_t* to = (uint16_t*)args.out + (row0 + r) * args.ldo;
+            const int64_t row = row_of(args, row0 + r);
+            const uint16_t* from = (const uint16_t*)args.base + row * args.ldb;
+            uint16_t* to = (uint16_t*)args.out + row * args.ldo;
             for (int64_t n = mine0; n < end + col * 8; n += kWideCols) {
                 if (n - col * 8 < whole) *(u32x4_any*)(to + n) = *(const u32x4_any*)(from + n);
                 else store_end(to, n, args.N, load_end(from, n, args.N));
@@ -716,7 +858,7 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
                               (tile_rows >> (g * 4 + 3) & 1) != 0};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // other rows read what one of the adapter's reads
-            const int64_t row = tile0 + (mine[j] ? g * 4 + j : one_row);
+            const int64_t row = row_of(args, tile0 + (mine[j] ? g * 4 + j : one_row));
             base[j] = (const uint16_t*)args.base + row * args.ldb + mine0;
             out[j] = (uint16_t*)args.out + row * args.ldo + mine0;
         }
@@ -734,10 +876,15 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
                 if (first + j * kWideCols < whole)
                     load_base_run(y[j], first + j * kWideCols);
             const int64_t row = tile0 + (tile_rows >> col & 1 ? col : one_row);
-            const float by = make_operands<KH>(high, low, args, row, adapter, g);
+            const uint16_t* h = args.operands + row * (KH * 64) + g * 8;
+#pragma unroll
+            for (int kh = 0; kh < KH; ++kh) {
+                high[kh] = *(const u32x4*)(h + kh * 32);
+                low[kh] = *(const u32x4*)(h + (KH + kh) * 32);
+            }
             if constexpr (!BF16)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) back[j] = __shfl(by, g * 4 + j, 64);
+                for (int j = 0; j < 4; ++j) back[j] = args.back[tile0 + (mine[j] ? g * 4 + j : one_row)];
         }
         for (int64_t n0 = first; n0 < end;) {
 #pragma unroll
@@ -820,6 +967,7 @@ hipError_t up(const LoraArgs& a, hipStream_t stream) {
     if (a.many) {
         const int64_t cols = (int64_t)kWideCols * a.up_each;
         const int64_t blocks = (a.N + cols - 1) / cols;
+        join_kernel<KH><<<(unsigned)((a.M + 15) / 16), 256, 0, stream>>>(a);
         up_wide_kernel<KH><<<(unsigned)((a.M + 63) / 64 * ((blocks + 7) / 8 * 8)), 256, 0, stream>>>(a);
     } else {
         const int64_t cols = (int64_t)kUpCols * (kUpWaves / a.up_wide) * a.up_each;
@@ -844,6 +992,7 @@ hipError_t up_any(const LoraArgs& a, hipStream_t stream) {
 }
 
 hipError_t both(const LoraArgs& a, bool x_fp8, hipStream_t stream) {
+    if (a.order) sort_kernel<<<1, 1024, 0, stream>>>(a);
     const hipError_t e = x_fp8 ? down_any<true>(a, stream) : down_any<false>(a, stream);
     return e == hipSuccess ? up_any(a, stream) : e;
 }

@@ -40,31 +40,53 @@ bool stride_ok(int64_t ld, int64_t W, int64_t M) {
 void set_plan(LoraArgs& a) {
     const int steps = (int)ceil_div(a.K, kStep);
     a.many = a.M >= 512;
-    // first product: K in parts until there is a workgroup for every CU
-    const int64_t groups = ceil_div(a.M, a.many ? 64 : 16) * rank_slices(a.R);
+    a.by_adapter = a.M >= 128;
+    // first product: K in parts until there is a workgroup for every CU; where every wave of
+    // the second product adds the parts up itself, no more than pay for that
+    const int64_t tiles = ceil_div(a.M, a.many ? 64 : 16), slices = rank_slices(a.R);
     a.splits = (int32_t)std::clamp<int64_t>(
-        256 / groups, 1, std::min<int64_t>(ceil_div(steps, a.many ? 4 : kDownWaves), 16));
-    const int64_t most = std::min<int64_t>(16, std::min<int64_t>(a.L, a.M));
-    a.down_z = (int32_t)std::clamp<int64_t>(512 / (groups * a.splits), 1, most);
+        a.many ? 256 / (tiles * slices) : std::max<int64_t>(16 / tiles, 4), 1,
+        std::min<int64_t>(ceil_div(steps, a.many ? 4 : kDownWaves), 16));
+    // adapters that a group of 16 rows may hold, in the mean if the rows are ordered
+    const int64_t most = std::min<int64_t>(
+        {a.L, a.M, 16, a.by_adapter ? 1 + ceil_div(16 * (int64_t)a.L, a.M) : 16});
+    a.down_z = (int32_t)std::clamp<int64_t>(1024 / (tiles * slices * a.splits), 1, most);
     // second product
     const int64_t runs = ceil_div(a.N, a.many ? 128 : kUpCols);
-    const int64_t tiles = ceil_div(a.M, a.many ? 64 : 16);
     if (a.many) {
-        // two workgroups per CU, twice, in blocks of columns that the 8 XCDs share evenly
-        const int64_t blocks = std::clamp<int64_t>(1024 / tiles / 8 * 8, 8, runs);
-        a.up_each = (int32_t)ceil_div(runs, blocks);
+        // runs of columns per workgroup: few rounds of the workgroups that the chip holds at
+        // once (two per CU up to 96 ranks), of which each costs three runs besides its own
+        const int64_t held = a.R <= 96 ? 512 : 256;
+        int64_t best = 0;
+        for (int64_t each = 1; each <= 16; ++each) {
+            const int64_t rounds = ceil_div(tiles * ceil_div(runs, each), held);
+            if (best == 0 || rounds * (each + 3) < best) {
+                best = rounds * (each + 3);
+                a.up_each = (int32_t)each;
+            }
+        }
         a.up_z = a.up_wide = 1;
         return;
     }
     a.up_wide = tiles >= 8 ? 4 : 1;
-    a.up_each = (int32_t)std::clamp<int64_t>(tiles * runs / 8192, 1, 16);
-    if (a.N >= (int64_t)1 << 23) a.up_each = 16;   // the grid's second dimension stays below 2^16
+    a.up_each = (int32_t)std::clamp<int64_t>(tiles * runs / 448, 1, 4);
+    if (a.N >= (int64_t)1 << 23) a.up_each = 4;   // the grid's second dimension stays below 2^16
     const int64_t waves = tiles * ceil_div(runs, a.up_each);
-    a.up_z = (int32_t)std::clamp<int64_t>(4096 / waves, 1, most);
+    a.up_z = (int32_t)std::clamp<int64_t>(8192 / waves, 1, most);
 }
 
-size_t bytes_of(const LoraArgs& a) {
-    return (size_t)kSkip + (size_t)a.splits * (size_t)a.M * (size_t)a.R * 4;
+// Offsets of the scratch behind kSkip.
+struct Scratch {
+    int64_t operands, back, order, bytes;
+};
+
+Scratch scratch_of(const LoraArgs& a) {
+    Scratch s;
+    s.operands = a.splits * a.M * a.R * 4;
+    s.back = s.operands + (a.many ? a.M * ceil_div(a.R, 32) * 128 : 0);
+    s.order = s.back + (a.many ? a.M * 4 : 0);
+    s.bytes = kSkip + s.order + (a.by_adapter ? a.M * 8 : 0);
+    return s;
 }
 
 }  // namespace
@@ -80,7 +102,7 @@ size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, uint32_t
     LoraArgs a{};
     a.M = M, a.N = N, a.K = K, a.R = (int32_t)R, a.L = 1;
     set_plan(a);
-    return bytes_of(a);
+    return (size_t)scratch_of(a).bytes;
 }
 
 w4a16_status_t lora_add(const void* base, int64_t ldb, const void* x, int64_t ldx,
@@ -106,9 +128,17 @@ w4a16_status_t lora_add(const void* base, int64_t ldb, const void* x, int64_t ld
     a.ldb = ldb, a.ldx = ldx, a.ldo = ldo, a.M = M, a.N = N, a.K = K;
     a.R = (int32_t)R, a.L = (int32_t)L, a.KB = (int32_t)ceil_div(K, 128);
     set_plan(a);
-    if (!workspace || workspace_bytes < bytes_of(a)) return W4A16_ERR_WORKSPACE;
+    const Scratch need = scratch_of(a);
+    if (!workspace || workspace_bytes < (size_t)need.bytes) return W4A16_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return W4A16_ERR_INVALID_ARG;
-    a.h = (float*)((uint8_t*)workspace + kSkip);
+    uint8_t* scratch = (uint8_t*)workspace + kSkip;
+    a.h = (float*)scratch;
+    a.operands = (uint16_t*)(scratch + need.operands);
+    a.back = (float*)(scratch + need.back);
+    if (a.by_adapter && L > 1) {
+        a.order = (int32_t*)(scratch + need.order);
+        a.sorted = a.order + M;
+    }
     return from_hip(flags & LORA_BF16 ? launch_bf16(a, fp8, (hipStream_t)stream)
                                       : launch_f16(a, fp8, (hipStream_t)stream));
 }

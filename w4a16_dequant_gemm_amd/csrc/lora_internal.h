@@ -24,10 +24,17 @@ struct LoraArgs {
     const float* scale;   // may be null
     const int32_t* ids;
     void* out;
+    int32_t* order;       // [M] rows by adapter (null: as they are), and their ids
+    int32_t* sorted;
     float* h;             // [splits][M][R]: partial inner products with A
+    // many rows: operands of the second product, [M][2][R filled up to 32], and (fp16) what
+    // a row's products are multiplied by
+    uint16_t* operands;
+    float* back;
     int64_t ldb, ldx, ldo, M, N, K;
     int32_t R, L, KB;     // KB: fp8 scales per row
     int32_t many;         // the forms for many rows
+    int32_t by_adapter;   // order the rows first
     int32_t splits;       // parts of K over workgroups
     int32_t down_z;       // workgroups that share a row group's adapters
     int32_t up_wide;      // waves of a workgroup of the second product side by side in rows: 4 or 1
