@@ -233,6 +233,18 @@ class Strided(FakeTensor):
         return 1
 
 
+class Buffer(FakeTensor):
+    """One allocation that several outputs are parts of."""
+
+    def as_strided(self, shape, strides, first):
+        assert strides == (1,) or strides == (shape[1], 1)
+        assert first + torch.Size(shape).numel() <= self.numel()
+        return Buffer(*shape, dtype=self.dtype)
+
+    def view(self, dtype):
+        return Buffer(*self.shape, dtype=dtype)
+
+
 @pytest.fixture
 def bound(monkeypatch):
     from w4a16_dequant_gemm_amd import lora, route
@@ -243,7 +255,7 @@ def bound(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(w4, "_stream_handle", lambda stream: 0)
     monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None:
-                        FakeTensor(*((shape,) if isinstance(shape, int) else shape), dtype=dtype))
+                        Buffer(*((shape,) if isinstance(shape, int) else shape), dtype=dtype))
     return route, lora
 
 

@@ -18,7 +18,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int kPiece = 8;   // elements per lane
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBackThreads = 512;   // at most
 
 template <bool BF16>
 __device__ __forceinline__ float to_float(uint32_t h) {
@@ -37,41 +37,58 @@ __device__ __forceinline__ float element(u32x4 q, int i) {
     return to_float<BF16>((i & 1) ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu);
 }
 
-// Elements n .. n+7 of a row of N; those behind the row's end are zeros.
+// A lane's 8 columns.  The last lane of a row of N >= 8 takes its last 8, of which the
+// first `skip` are the lane's before it: loads need no condition.  SHORT: N < 8, one lane.
+struct Columns {
+    int64_t n;
+    int skip;
+};
+
+template <bool SHORT>
+__device__ __forceinline__ Columns columns(int64_t first, int64_t N) {
+    if (SHORT) return {0, 0};
+    const int64_t n = min(first, N - kPiece);
+    return {n, (int)(first - n)};
+}
+
+template <bool SHORT>
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int64_t n, int64_t N) {
-    if (n + kPiece <= N) return __builtin_nontemporal_load((const u32x4_any*)(row + n));
+    if constexpr (!SHORT) return __builtin_nontemporal_load((const u32x4_any*)(row + n));
     u32x4 q = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < kPiece; ++i)
-        if (n + i < N) q[i / 2] |= (uint32_t)row[n + i] << (16 * (i & 1));
+        if (i < N) q[i / 2] |= (uint32_t)row[i] << (16 * (i & 1));
     return q;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t n, int64_t N,
+// Writes the lane's own columns only.
+template <bool BF16, bool SHORT>
+__device__ __forceinline__ void store8(uint16_t* row, Columns c, int64_t N,
                                        const float (&v)[kPiece]) {
-    if (n + kPiece <= N) {
+    if (!SHORT && c.skip == 0) {
         u32x4 q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = to_half<BF16>(v[2 * i]) | to_half<BF16>(v[2 * i + 1]) << 16;
-        *(u32x4_any*)(row + n) = q;
+        *(u32x4_any*)(row + c.n) = q;
     } else {
 #pragma unroll
         for (int i = 0; i < kPiece; ++i)
-            if (n + i < N) row[n + i] = (uint16_t)to_half<BF16>(v[i]);
+            if (i >= c.skip && c.n + i < N) row[c.n + i] = (uint16_t)to_half<BF16>(v[i]);
     }
 }
 
 // Workgroup (token, run of columns).  The rows of up to JG slots are in flight at once.
-template <bool BF16, int JG>
+template <bool BF16, int JG, bool SHORT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
     const int64_t t = a.first + blockIdx.x;
-    const int64_t n = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * kPiece;
-    if (n >= a.N) return;
+    const int64_t first = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * kPiece;
+    if (first >= a.N) return;
+    const Columns c = columns<SHORT>(first, a.N);
     const float* weights = a.weights + t * a.top;
     const int32_t* places = a.places + t * a.top;
     float acc[kPiece];
-    const u32x4 r = a.extra ? load8((const uint16_t*)a.extra + t * a.lde, n, a.N) : u32x4{0, 0, 0, 0};
+    u32x4 r = {0u, 0u, 0u, 0u};
+    if (a.extra) r = load8<SHORT>((const uint16_t*)a.extra + t * a.lde, c.n, a.N);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) acc[i] = element<BF16>(r, i);
     for (int j0 = 0; j0 < a.top; j0 += JG) {
@@ -81,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
         for (int j = 0; j < JG; ++j) {
             const int64_t p = j0 + j < a.top ? places[j0 + j] : -1;
             there[j] = p >= 0 && p < a.R;
-            if (there[j]) q[j] = load8((const uint16_t*)a.y + p * a.ldy, n, a.N);
+            if (there[j]) q[j] = load8<SHORT>((const uint16_t*)a.y + p * a.ldy, c.n, a.N);
         }
 #pragma unroll
         for (int j = 0; j < JG; ++j) {
@@ -92,18 +109,19 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
                 acc[i] = __builtin_fmaf(w, element<BF16>(q[j], i), acc[i]);
         }
     }
-    store8<BF16>((uint16_t*)a.out + t * a.N, n, a.N, acc);
+    store8<BF16, SHORT>((uint16_t*)a.out + t * a.N, c, a.N, acc);
 }
 
 // A workgroup per token: the whole inner products lie in it.
-template <bool BF16, int JG>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs a) {
-    __shared__ float part[kThreads / 64][JG];
+template <bool BF16, int JG, bool SHORT>
+__global__ __launch_bounds__(kBackThreads) void combine_backward_kernel(CombineArgs a) {
+    __shared__ float part[kBackThreads / 64][JG];
     const int64_t t = a.first + blockIdx.x;
     const float* weights = a.weights + t * a.top;
     const int32_t* places = a.places + t * a.top;
     const uint16_t* dout = (const uint16_t*)a.extra + t * a.lde;
     const int64_t routed = a.routed ? min((int64_t)max(*a.routed, 0), a.R) : a.R;
+    const int64_t stride = (int64_t)blockDim.x * kPiece;
     for (int j0 = 0; j0 < a.top; j0 += JG) {
         int64_t place[JG];
         float w[JG], dot[JG];
@@ -114,12 +132,14 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
             w[j] = place[j] >= 0 ? weights[j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int64_t n = (int64_t)threadIdx.x * kPiece; n < a.N; n += kThreads * kPiece) {
-            const u32x4 d = load8(dout, n, a.N);
+        for (int64_t first = (int64_t)threadIdx.x * kPiece; first < a.N; first += stride) {
+            const Columns c = columns<SHORT>(first, a.N);
+            const u32x4 d = load8<SHORT>(dout, c.n, a.N);
             u32x4 q[JG];
 #pragma unroll
             for (int j = 0; j < JG; ++j)
-                if (place[j] >= 0) q[j] = load8((const uint16_t*)a.y + place[j] * a.ldy, n, a.N);
+                if (place[j] >= 0)
+                    q[j] = load8<SHORT>((const uint16_t*)a.y + place[j] * a.ldy, c.n, a.N);
 #pragma unroll
             for (int j = 0; j < JG; ++j) {
                 if (place[j] < 0) continue;
@@ -127,10 +147,11 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
 #pragma unroll
                 for (int i = 0; i < kPiece; ++i) {
                     const float x = element<BF16>(d, i);
-                    dot[j] = __builtin_fmaf(x, element<BF16>(q[j], i), dot[j]);
+                    const float y = i >= c.skip ? element<BF16>(q[j], i) : 0.0f;
+                    dot[j] = __builtin_fmaf(i >= c.skip ? x : 0.0f, y, dot[j]);
                     v[i] = x * w[j];
                 }
-                store8<BF16>((uint16_t*)a.out + place[j] * a.N, n, a.N, v);
+                store8<BF16, SHORT>((uint16_t*)a.out + place[j] * a.N, c, a.N, v);
             }
         }
 #pragma unroll
@@ -142,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
         __syncthreads();
         if (threadIdx.x < JG && j0 + (int)threadIdx.x < a.top) {
             float sum = part[0][threadIdx.x];
-            for (int k = 1; k < kThreads / 64; ++k) sum += part[k][threadIdx.x];
+            for (int k = 1; k < (int)blockDim.x / 64; ++k) sum += part[k][threadIdx.x];
             a.dweights[t * a.top + j0 + threadIdx.x] = sum;
         }
         __syncthreads();
@@ -152,48 +173,68 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
         const int64_t to = min((t + 1) * a.top, a.R);
         const float zeros[kPiece] = {};
         for (int64_t row = from; row < to; ++row)
-            for (int64_t n = (int64_t)threadIdx.x * kPiece; n < a.N; n += kThreads * kPiece)
-                store8<BF16>((uint16_t*)a.out + row * a.N, n, a.N, zeros);
+            for (int64_t first = (int64_t)threadIdx.x * kPiece; first < a.N; first += stride)
+                store8<BF16, SHORT>((uint16_t*)a.out + row * a.N, columns<SHORT>(first, a.N), a.N,
+                                    zeros);
     }
 }
 
-
 // HIP counts a launch's work-items with 32 bits.
-constexpr int64_t kMostGroups = 1 << 23;
+constexpr int64_t kMostGroups = 1 << 22;
+
+// Workgroups of at most `most` lanes share a row's pieces out evenly.
+struct Split {
+    int64_t runs;
+    int threads;
+};
+
+Split split_of(int64_t N, int most) {
+    const int64_t pieces = (N + kPiece - 1) / kPiece, runs = (pieces + most - 1) / most;
+    return {runs, (int)(((pieces + runs - 1) / runs + 63) / 64 * 64)};
+}
 
 template <bool BF16, int JG>
 hipError_t combine(CombineArgs a, hipStream_t stream) {
-    const int64_t runs = (a.N + kThreads * kPiece - 1) / (kThreads * kPiece);
-    const int64_t most = kMostGroups / runs;
+    const Split by = split_of(a.N, kThreads);
+    const int64_t most = kMostGroups / by.runs;
     for (a.first = 0; a.first < a.T; a.first += most) {
-        const dim3 grid((unsigned)min(a.T - a.first, most), (unsigned)runs);
-        combine_kernel<BF16, JG><<<grid, kThreads, 0, stream>>>(a);
+        const dim3 grid((unsigned)min(a.T - a.first, most), (unsigned)by.runs);
+        if (a.N < kPiece)
+            combine_kernel<BF16, JG, true><<<grid, 64, 0, stream>>>(a);
+        else
+            combine_kernel<BF16, JG, false><<<grid, by.threads, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
 
 template <bool BF16, int JG>
 hipError_t combine_backward(CombineArgs a, hipStream_t stream) {
-    for (a.first = 0; a.first < a.T; a.first += kMostGroups)
-        combine_backward_kernel<BF16, JG>
-            <<<(unsigned)min(a.T - a.first, kMostGroups), kThreads, 0, stream>>>(a);
+    const int threads = split_of(a.N, kBackThreads).threads;
+    for (a.first = 0; a.first < a.T; a.first += kMostGroups) {
+        const unsigned groups = (unsigned)min(a.T - a.first, kMostGroups);
+        if (a.N < kPiece)
+            combine_backward_kernel<BF16, JG, true><<<groups, 64, 0, stream>>>(a);
+        else
+            combine_backward_kernel<BF16, JG, false><<<groups, threads, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
+#define COMBINE_BY_TOP(f)                       \
+    (a.top == 1   ? f<BF16, 1>(a, stream)       \
+     : a.top == 2 ? f<BF16, 2>(a, stream)       \
+     : a.top <= 4 ? f<BF16, 4>(a, stream)       \
+     : a.top <= 6 ? f<BF16, 6>(a, stream)       \
+                  : f<BF16, 8>(a, stream))
+
 template <bool BF16>
 hipError_t combine_any(const CombineArgs& a, hipStream_t stream) {
-    if (a.top == 1) return combine<BF16, 1>(a, stream);
-    if (a.top == 2) return combine<BF16, 2>(a, stream);
-    if (a.top <= 4) return combine<BF16, 4>(a, stream);
-    return combine<BF16, 8>(a, stream);
+    return COMBINE_BY_TOP(combine);
 }
 
 template <bool BF16>
 hipError_t combine_backward_any(const CombineArgs& a, hipStream_t stream) {
-    if (a.top == 1) return combine_backward<BF16, 1>(a, stream);
-    if (a.top == 2) return combine_backward<BF16, 2>(a, stream);
-    if (a.top <= 4) return combine_backward<BF16, 4>(a, stream);
-    return combine_backward<BF16, 8>(a, stream);
+    return COMBINE_BY_TOP(combine_backward);
 }
 
 }  // namespace

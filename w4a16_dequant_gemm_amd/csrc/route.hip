@@ -70,6 +70,24 @@ __device__ __forceinline__ float group_max(float x) {
     return x;
 }
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_bits(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xF, 0xF, false);
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t group_max_bits(uint32_t x) {
+    x = max(x, dpp_bits<kXor1>(x));
+    x = max(x, dpp_bits<kXor2>(x));
+    x = max(x, dpp_bits<kHalfMirror>(x));
+    x = max(x, dpp_bits<kMirror>(x));
+    if constexpr (G == 64) {
+        x = max(x, (uint32_t)__shfl_xor((int)x, 16, 64));
+        x = max(x, (uint32_t)__shfl_xor((int)x, 32, 64));
+    }
+    return x;
+}
+
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
     x += dpp<kXor1>(x);
@@ -90,6 +108,80 @@ __device__ __forceinline__ int group_min(int x) {
     return x;
 }
 
+template <int G>
+__device__ __forceinline__ float group_min(float x) {
+    return -group_max<G>(-x);
+}
+
+// ---- 16 lanes: prefix sums and all pairs
+
+constexpr int kShr = 0x110, kRor = 0x120;   // by 1 to 15 lanes
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_or_zero(int x) {   // 0 where the row has no such lane
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, 0xF, 0xF, false);
+}
+
+__device__ __forceinline__ int dpp_last(int x) {   // that of lane 15 in every lane
+    return __shfl(x, 15, 16);
+}
+
+template <int BY, typename F>
+__device__ __forceinline__ void for_one(float x, F f) {
+    f(dpp<kRor + BY>(x));
+}
+
+template <int BY, typename F>
+__device__ __forceinline__ void for_one(uint32_t x, F f) {
+    f(dpp_bits<kRor + BY>(x));
+}
+
+template <int BY, typename F>
+__device__ __forceinline__ void for_one(uint64_t x, F f) {
+    f((uint64_t)dpp_bits<kRor + BY>((uint32_t)(x >> 32)) << 32 | dpp_bits<kRor + BY>((uint32_t)x));
+}
+
+// f of the 15 other lanes' x, in whichever order.
+template <typename T, typename F>
+__device__ __forceinline__ void for_others(T x, F f) {
+    for_one<1>(x, f), for_one<2>(x, f), for_one<3>(x, f), for_one<4>(x, f), for_one<5>(x, f);
+    for_one<6>(x, f), for_one<7>(x, f), for_one<8>(x, f), for_one<9>(x, f), for_one<10>(x, f);
+    for_one<11>(x, f), for_one<12>(x, f), for_one<13>(x, f), for_one<14>(x, f), for_one<15>(x, f);
+}
+
+// A logit and its expert as one whole number, the larger the earlier it is chosen; above 0.
+#if ROUTE_TU_TYPE == 2
+typedef uint64_t Key;
+
+__device__ __forceinline__ Key key_of(float l, int e) {
+    const int b = __float_as_int(l + 0.0f);   // -0 + 0 is +0
+    return (uint64_t)((uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u)) << 32 |
+           (0xFFFFFFFFu - (uint32_t)e);
+}
+#else
+typedef uint32_t Key;
+
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = to_bits(v + 0.0f);   // -0 + 0 is +0
+    return (b & 0x8000u) ? b ^ 0xFFFFu : b | 0x8000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return from_bits((k & 0x8000u) ? k ^ 0x8000u : k ^ 0xFFFFu);
+}
+
+__device__ __forceinline__ Key key_of(float l, int e) {
+    return ordered(l) << 16 | (0xFFFFu - (uint32_t)e);
+}
+#endif
+
+// What the wave's lanes wrote to LDS is there for all of them.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- a token's row in registers: lane g holds runs of kRun consecutive elements
 
 template <int G, int PER>
@@ -106,39 +198,36 @@ struct Row {
                                                 int E, int g, bool wide) {
         const uint8_t* p = (const uint8_t*)base + row_at * kBytes;
 #pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = -kInf;
+#pragma unroll
         for (int c = 0; c < PER / kRun; ++c) {
             const int e0 = (c * G + g) * kRun;
             if (wide) {   // E is a multiple of kVec: a run is inside or outside as a whole
+                if (e0 >= E) continue;
                 uint32_t w[(kRun * kBytes + 3) / 4];
-                if (e0 < E) {
-                    if constexpr (kRun * kBytes == 16) {
-                        const u32x4 q = *(const u32x4*)(p + e0 * kBytes);
+                if constexpr (kRun * kBytes == 16) {
+                    const u32x4 q = *(const u32x4*)(p + e0 * kBytes);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = q[k];
-                    } else if constexpr (kRun * kBytes == 8) {
-                        const u32x2 q = *(const u32x2*)(p + e0 * kBytes);
-                        w[0] = q[0], w[1] = q[1];
-                    } else if constexpr (kRun * kBytes == 4) {
-                        w[0] = *(const uint32_t*)(p + e0 * kBytes);
-                    } else {
-                        w[0] = *(const uint16_t*)(p + e0 * kBytes);
-                    }
+                    for (int k = 0; k < 4; ++k) w[k] = q[k];
+                } else if constexpr (kRun * kBytes == 8) {
+                    const u32x2 q = *(const u32x2*)(p + e0 * kBytes);
+                    w[0] = q[0], w[1] = q[1];
+                } else if constexpr (kRun * kBytes == 4) {
+                    w[0] = *(const uint32_t*)(p + e0 * kBytes);
+                } else {
+                    w[0] = *(const uint16_t*)(p + e0 * kBytes);
                 }
 #pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    const uint32_t b = TYPE == 2 ? w[k] : (k & 1) ? w[k / 2] >> 16
-                                                                  : w[k / 2] & 0xFFFFu;
-                    v[c * kRun + k] = e0 < E ? from_bits(b) : -kInf;
-                }
+                for (int k = 0; k < kRun; ++k)
+                    v[c * kRun + k] = from_bits(TYPE == 2   ? w[k]
+                                                : (k & 1) ? w[k / 2] >> 16
+                                                          : w[k / 2] & 0xFFFFu);
             } else {
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
-                    float x = -kInf;
-                    if (e0 + k < E) {
-                        if constexpr (TYPE == 2) x = ((const float*)p)[e0 + k];
-                        else x = from_bits(((const uint16_t*)p)[e0 + k]);
-                    }
-                    v[c * kRun + k] = x;
+                    if (e0 + k >= E) continue;
+                    if constexpr (TYPE == 2) v[c * kRun + k] = ((const float*)p)[e0 + k];
+                    else v[c * kRun + k] = from_bits(((const uint16_t*)p)[e0 + k]);
                 }
             }
         }
@@ -180,12 +269,10 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ float no_nan(float x) { return x == x ? x : -kInf; }
-
 // exp(x) for x <= 0 or NaN: below -104 it is 0 in fp32 (and exp_scaled is not for
 // -infinity).
 __device__ __forceinline__ float exp_down(float x) {
-    return x < -104.0f ? 0.0f : exp_scaled(x, 0.0f);
+    return exp_scaled(__builtin_elementwise_maximum(x, -110.0f), 0.0f);   // NaN stays
 }
 
 // The maximum to subtract, v into exp(v - maximum), their sum.
@@ -236,24 +323,24 @@ __device__ int scan_counts(int* count, int n, int* part) {
     return total;
 }
 
-// The loss and pull from the counts and the sums of p: one workgroup.
-__device__ void finish_loss(const RouteArgs& a, const int32_t* counts, const float* sums, int V,
-                            float* part) {
+// The loss and pull from the counts and the sums of p of every expert: one workgroup.
+template <typename Count, typename Sum>
+__device__ void finish_loss(const RouteArgs& a, int V, float* part, Count count, Sum sum) {
     const double unit = V > 0 ? (double)a.E / ((double)V * a.top) / V : 0.0;
     float mine = 0.0f;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        const float pull = (float)(counts[e] * unit);
+        const float pull = (float)(count(e) * unit);
         a.pull[e] = pull;
-        mine += V > 0 ? pull * sums[e] : 0.0f;
+        mine += V > 0 ? pull * sum(e) : 0.0f;
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) mine += __shfl_xor(mine, off, 64);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float sum = 0.0f;
-        for (int w = 0; w < (int)blockDim.x / 64; ++w) sum += part[w];
-        *a.loss = sum;
+        float all = 0.0f;
+        for (int w = 0; w < (int)blockDim.x / 64; ++w) all += part[w];
+        *a.loss = all;
     }
 }
 
@@ -275,10 +362,13 @@ __host__ __device__ inline Shared shared_of(int E, int top, int tile, int thread
     return s;
 }
 
+constexpr int kOneThreads = 512, kTileThreads = 256;
+
 // One workgroup per tile of tokens.  ONE: there is one tile, and the outputs are final.
 template <int G, int PER, bool LOSS, bool ONE>
-__global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
+__global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_kernel(RouteArgs a) {
     extern __shared__ uint8_t lds[];
+    __shared__ u32x2 slots[G == 16 ? kOneThreads : 1];   // candidates, 16 for each group of lanes
     const int E = a.E, top = a.top, threads = blockDim.x;
     const Shared at = shared_of(E, top, a.tile, threads, LOSS);
     unsigned long long* mask = (unsigned long long*)lds;
@@ -305,15 +395,10 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
         const int t = round + group;
         const bool live = t < here && (!a.valid || a.valid[first + t]);
         float v[PER], p[PER];
-        if (live) {
-            Row<G, PER>::load(v, a.logits, (first + t) * a.ld, E, g, a.wide);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) v[i] = -kInf;
-        }
+        Row<G, PER>::load(v, a.logits, (first + t) * a.ld, live ? E : 0, g, a.wide);
         float best = -kInf;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = fmaxf(best, no_nan(v[i]));
+        for (int i = 0; i < PER; ++i) best = fmaxf(best, v[i]);   // not a NaN
         float high = group_max<G>(best);
         const float base = high == -kInf ? 0.0f : high;
         const float sum = exps<G, PER>(v, p, high);
@@ -322,42 +407,121 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) sums[i] = __builtin_fmaf(p[i], inv, sums[i]);
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = no_nan(v[i]);
         float taken = 0.0f;
-        for (int j = 0; j < top; ++j) {
-            // the first of this lane's elements that equal the group's largest
-            int i_win = PER;
-#pragma unroll
-            for (int i = PER - 1; i >= 0; --i) i_win = v[i] == high ? i : i_win;
-            bool win = i_win < PER && high > -kInf;
-            const int e = Row<G, PER>::at(i_win, g);
-            const unsigned long long winners = __ballot(win);
-            const unsigned long long ours = G == 64 ? winners : (winners >> (lane & 48)) & 0xFFFFu;
-            if (__any(__popcll(ours) > 1)) {   // equal logits on several lanes: the lowest index
-                const int lowest = group_min<G>(win ? e : 0x7FFFFFFF);
-                win = win && e == lowest;
-            }
-            const float x = high > -kInf ? exp_down(high - base) : 0.0f;
+        auto choose = [&](int j, bool win, int e, float l) {   // l: the chosen logit, the group's
+            const float x = l > -kInf ? exp_down(l - base) : 0.0f;
             taken += x;
-            if (t < here) {
-                if (win) {
-                    chosen[t * top + j] = (uint16_t)e;
-                    weight[t * top + j] = x;
-                    atomicOr(&mask[e], 1ull << t);
-                } else if (high == -kInf && g == 0) {
-                    chosen[t * top + j] = kNone;
+            if (t >= here) return;
+            if (win) {
+                chosen[t * top + j] = (uint16_t)e;
+                weight[t * top + j] = x;
+                atomicOr(&mask[e], 1ull << t);
+            } else if (l == -kInf && g == 0) {
+                chosen[t * top + j] = kNone;
+            }
+        };
+        // Few logits can be among the top: the top-th largest of the lanes' largest bounds
+        // them from below, and little else is not below it (11 of 256 logits for the 8
+        // largest).  If that is at most one for each lane it goes there through LDS, and
+        // a candidate's place is the number of larger ones: a third of the arithmetic
+        // of the rounds below, which find one after the other.
+        bool done = false;
+        if constexpr (G == 16) {
+            if (top <= 8) {
+                int above = 0;
+                for_others(best, [&](float other) { above += other > best; });
+                const float bound = group_min<G>(above < top ? best : kInf);
+                int mine = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) mine += v[i] >= bound;
+                int upto = mine;
+                upto += dpp_or_zero<kShr + 1>(upto);
+                upto += dpp_or_zero<kShr + 2>(upto);
+                upto += dpp_or_zero<kShr + 4>(upto);
+                upto += dpp_or_zero<kShr + 8>(upto);
+                // -infinity: fewer lanes than top hold a logit that can be chosen
+                done = __all(!live || (bound > -kInf && upto <= 16));
+                if (done) {
+                    u32x2* slot = slots + threadIdx.x / 16 * 16;
+                    slot[g] = u32x2{0u, 0u};
+                    wave_sync();
+                    if (live) {
+                        int at = upto - mine;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            if (v[i] >= bound)
+                                slot[at++] = u32x2{(uint32_t)Row<G, PER>::at(i, g), to_bits(v[i])};
+                    }
+                    wave_sync();
+                    const u32x2 candidate = slot[g];
+                    const int e = (int)candidate[0];
+                    const float l = from_bits(candidate[1]);
+                    const bool any = live && g < dpp_last(upto);
+                    const Key key = any ? key_of(l, e) : 0;
+                    int place = 0;
+                    for_others(key, [&](Key other) { place += other > key; });
+                    const bool win = any && place < top;
+                    const float x = win ? exp_down(l - base) : 0.0f;
+                    taken = group_sum<G>(x);
+                    if (win) {
+                        chosen[t * top + place] = (uint16_t)e;
+                        weight[t * top + place] = x;
+                        atomicOr(&mask[e], 1ull << t);
+                    } else if (!live && t < here && g < top) {
+                        chosen[t * top + g] = kNone;
+                    }
+                    wave_sync();   // the next token's candidates use the same slots
                 }
             }
-            if (j + 1 == top) break;
-            const int gone = win ? i_win : PER;
-            best = -kInf;
+        }
+        if (!done) {
+#if ROUTE_TU_TYPE != 2
+            // one maximum finds the logit and its index, and no two keys are equal
+            uint32_t key[PER], most = 0;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                v[i] = i == gone ? -kInf : v[i];
-                best = fmaxf(best, v[i]);
+                key[i] = v[i] > -kInf ? key_of(v[i], Row<G, PER>::at(i, g)) : 0u;
+                most = max(most, key[i]);
             }
-            high = group_max<G>(best);
+            for (int j = 0; j < top; ++j) {
+                const uint32_t first = group_max_bits<G>(most);
+                choose(j, most == first && first != 0, 0xFFFF - (int)(first & 0xFFFFu),
+                       first != 0 ? unordered(first >> 16) : -kInf);
+                if (j + 1 == top) break;
+                most = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    key[i] = key[i] == first ? 0u : key[i];
+                    most = max(most, key[i]);
+                }
+            }
+#else
+            for (int j = 0; j < top; ++j) {
+                // the first of this lane's elements that equal the group's largest
+                int i_win = PER;
+#pragma unroll
+                for (int i = PER - 1; i >= 0; --i) i_win = v[i] == high ? i : i_win;
+                bool win = i_win < PER && high > -kInf;
+                const int e = Row<G, PER>::at(i_win, g);
+                const unsigned long long winners = __ballot(win);
+                const unsigned long long ours =
+                    G == 64 ? winners : (winners >> (lane & 48)) & 0xFFFFu;
+                if (__any(__popcll(ours) > 1)) {   // equal logits on several lanes: the lowest index
+                    const int lowest = group_min<G>(win ? e : 0x7FFFFFFF);
+                    win = win && e == lowest;
+                }
+                choose(j, win, e, high);
+                if (j + 1 == top) break;
+                const int gone = win ? i_win : PER;
+                best = -kInf;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    v[i] = i == gone ? -kInf : v[i];
+                    best = fmaxf(best, v[i]);
+                }
+                high = group_max<G>(best);
+            }
+#endif
         }
         if (g == 0 && t < here) {
             // a NaN of the row is in sum
@@ -428,9 +592,8 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
     }
     if constexpr (ONE && LOSS) {
         __syncthreads();
-        for (int e = threadIdx.x; e < E; e += threads) offset[e] = __popcll(mask[e]);
-        __syncthreads();
-        finish_loss(a, offset, all, valid_here, (float*)part);
+        finish_loss(a, valid_here, (float*)part, [&](int e) { return __popcll(mask[e]); },
+                    [&](int e) { return all[e]; });
     }
 }
 
@@ -519,42 +682,105 @@ __global__ __launch_bounds__(kScanCols* kScanRuns) void sum_tiles_kernel(RouteAr
     }
     if (run == 0 && e <= E) {
         a.all_counts[e] = carry;
-        if (e < E) a.counts[e] = carry;
         if (LOSS && e < E) a.all_p[e] = all_p;
     }
 }
 
-constexpr int kPlaceThreads = 256, kPlaceEach = 4;
+constexpr int kPlaceThreads = 256;
+constexpr int kPlaceSlots = kTile * ROUTE_MAX_TOP / kPlaceThreads;       // of a tile, per thread
+constexpr int kPlaceCols = (ROUTE_MAX_EXPERTS + 1 + kPlaceThreads - 1) / kPlaceThreads;
 
-// Ranks within tiles into places; workgroup 0 also writes the offsets and the loss.
-template <bool LOSS>
+// Ranks within tiles into places: a workgroup per tile, and one more for the offsets and
+// the loss.  JOIN: few tiles, whose counts each workgroup adds up for itself (a launch
+// less: JOIN_US).
+template <bool LOSS, bool JOIN>
 __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
-    __shared__ int offset[ROUTE_MAX_EXPERTS];
+    __shared__ int base[ROUTE_MAX_EXPERTS + 1];
     __shared__ int part[kPlaceThreads / 64];
     const int E = a.E;
-    for (int e = threadIdx.x; e < E; e += kPlaceThreads) offset[e] = a.all_counts[e];
-    __syncthreads();
-    const int total = scan_counts(offset, E, part);
-    if (blockIdx.x == 0) {
-        for (int e = threadIdx.x; e < E; e += kPlaceThreads) a.offsets[e] = offset[e];
-        if (threadIdx.x == 0) a.offsets[E] = total;
-        if constexpr (LOSS) finish_loss(a, a.all_counts, a.all_p, a.all_counts[E], (float*)part);
-    }
-    const int64_t slots = a.T * a.top;
-    const int64_t from = (int64_t)blockIdx.x * (kPlaceThreads * kPlaceEach) + threadIdx.x;
+    const bool totals = blockIdx.x == 0;   // it has most to do
+    const int tile = (int)blockIdx.x - 1;
+    const int64_t first = (int64_t)tile * a.tile * a.top;   // not used by the one without a tile
+    const int slots = totals ? 0 : (int)min((int64_t)a.tile * a.top, a.T * a.top - first);
+    int expert[kPlaceSlots], rank[kPlaceSlots];
 #pragma unroll
-    for (int k = 0; k < kPlaceEach; ++k) {
-        const int64_t s = from + k * kPlaceThreads;
-        if (s >= slots) break;
-        const int e = a.experts[s];
-        if (e >= 0) {
-            const uint32_t t = (uint32_t)s / (uint32_t)a.top;
-            const uint32_t tile = t / (uint32_t)a.tile;
-            const int place = a.places[s] + offset[e] + a.tile_counts[(int64_t)tile * (E + 1) + e];
-            a.places[s] = place;
-            a.rows[place] = (int)t;
+    for (int k = 0; k < kPlaceSlots; ++k) {
+        const int s = threadIdx.x + k * kPlaceThreads;
+        expert[k] = s < slots ? a.experts[first + s] : -1;
+        rank[k] = s < slots ? a.places[first + s] : -1;
+    }
+    // over all tiles, and over those before this one; column E: valid tokens
+    int all[kPlaceCols], before[kPlaceCols];
+#pragma unroll
+    for (int c = 0; c < kPlaceCols; ++c) {
+        const int e = threadIdx.x + c * kPlaceThreads;
+        all[c] = before[c] = 0;
+        if (e > E) continue;
+        if constexpr (JOIN) {
+            for (int b0 = 0; b0 < a.tiles; b0 += 16) {
+                int n[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    n[i] = b0 + i < a.tiles ? a.tile_counts[(b0 + i) * (E + 1) + e] : 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    all[c] += n[i];
+                    before[c] += b0 + i < tile ? n[i] : 0;
+                }
+            }
+        } else {
+            all[c] = a.all_counts[e];
+            if (!totals && e < E) before[c] = a.tile_counts[(int64_t)tile * (E + 1) + e];
         }
-        if (s >= total) a.rows[s] = -1;
+        base[e] = all[c];
+    }
+    __syncthreads();
+    const int V = base[E];
+    const int total = scan_counts(base, E, part);
+    if (totals) {
+#pragma unroll
+        for (int c = 0; c < kPlaceCols; ++c) {
+            const int e = threadIdx.x + c * kPlaceThreads;
+            if (e < E) {
+                a.offsets[e] = base[e];
+                a.counts[e] = all[c];
+            }
+        }
+        if (threadIdx.x == 0) a.offsets[E] = total;
+        if constexpr (LOSS)
+            finish_loss(a, V, (float*)part,
+                        [&](int e) { return (e + 1 < E ? base[e + 1] : total) - base[e]; },
+                        [&](int e) {
+                            if constexpr (!JOIN) return a.all_p[e];
+                            float sum = 0.0f;
+                            for (int b0 = 0; b0 < a.tiles; b0 += 16) {
+                                float p[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    p[i] = b0 + i < a.tiles ? a.tile_p[(b0 + i) * E + e] : 0.0f;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum += p[i];
+                            }
+                            return sum;
+                        });
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kPlaceCols; ++c) {
+        const int e = threadIdx.x + c * kPlaceThreads;
+        if (e < E) base[e] += before[c];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPlaceSlots; ++k) {
+        const int s = threadIdx.x + k * kPlaceThreads;
+        if (s >= slots) break;
+        if (expert[k] >= 0) {
+            const int place = rank[k] + base[expert[k]];
+            a.places[first + s] = place;
+            a.rows[place] = tile * a.tile + s / a.top;
+        }
+        if (first + s >= total) a.rows[first + s] = -1;
     }
 }
 
@@ -568,85 +794,90 @@ constexpr int kBackThreads = 256;
 template <int G, int PER>
 __global__ __launch_bounds__(kBackThreads) void back_kernel(BackArgs a) {
     extern __shared__ uint8_t lds[];
+    typedef Row<G, PER> R;
+    typedef float Run __attribute__((ext_vector_type(R::kRun)));
     const int E = a.E, top = a.top;
     const int g = threadIdx.x % G, group = threadIdx.x / G;
-    const int64_t t = (int64_t)blockIdx.x * (kBackThreads / G) + group;
-    const bool inside = t < a.T;
-    const bool live = inside && (!a.valid || a.valid[t]);
-    float* extra = (float*)lds + group * E;
-    for (int e = g; e < E; e += G) extra[e] = 0.0f;
-    __syncthreads();
-
-    float v[PER], p[PER];
-    if (live) {
-        Row<G, PER>::load(v, a.logits, t * a.ld, E, g, a.wide);
-    } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = -kInf;
-    }
-    float shared = 0.0f;   // what every expert's p is multiplied by
-    if (a.dweights) {
-        float pulled = 0.0f;
-        if (live)
-            for (int j = g; j < top; j += G) {
-                const int e = a.experts[t * top + j];
-                if (e >= 0 && e < E)
-                    pulled = __builtin_fmaf(a.weights[t * top + j], a.dweights[t * top + j], pulled);
-            }
-        pulled = group_sum<G>(pulled);
-        if (live)
-            for (int j = g; j < top; j += G) {
-                const int e = a.experts[t * top + j];
-                const float w = a.weights[t * top + j], d = a.dweights[t * top + j];
-                if (e >= 0 && e < E) extra[e] = w * (a.renormalize ? d - pulled : d);
-            }
-        if (!a.renormalize) shared = pulled;
-    }
-    float high = -kInf;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) high = fmaxf(high, no_nan(v[i]));
-    high = group_max<G>(high);
-    const float inv = inverse(exps<G, PER>(v, p, high));
+    // a lane's elements lie where it reads them: runs in the order of its registers
+    float* extra = (float*)lds + group * (G * PER);
     float pull[PER];
     const float dloss = a.dloss ? *a.dloss : 0.0f;
-    if (a.dloss) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        pull[i] = a.dloss && R::at(i, g) < E ? a.pull[R::at(i, g)] : 0.0f;
+
+    const int64_t step = (int64_t)gridDim.x * (kBackThreads / G);
+    for (int64_t t = (int64_t)blockIdx.x * (kBackThreads / G) + group; t - group < a.T; t += step) {
+        const bool inside = t < a.T;
+        const bool live = inside && (!a.valid || a.valid[t]);
+        float v[PER], p[PER];
+        R::load(v, a.logits, t * a.ld, live ? E : 0, g, a.wide);
+        float shared = 0.0f;   // what every expert's p is multiplied by
+        if (a.dweights) {
+#pragma unroll
+            for (int c = 0; c < PER / R::kRun; ++c)
+                *(Run*)(extra + (c * G + g) * R::kRun) = Run(0.0f);
+            wave_sync();   // a token's lanes lie in one wave
+            float pulled = 0.0f;
+            if (live)
+                for (int j = g; j < top; j += G) {
+                    const int e = a.experts[t * top + j];
+                    if (e >= 0 && e < E)
+                        pulled = __builtin_fmaf(a.weights[t * top + j], a.dweights[t * top + j],
+                                                pulled);
+                }
+            pulled = group_sum<G>(pulled);
+            if (live)
+                for (int j = g; j < top; j += G) {
+                    const int e = a.experts[t * top + j];
+                    const float w = a.weights[t * top + j], d = a.dweights[t * top + j];
+                    if (e >= 0 && e < E) extra[e] = w * (a.renormalize ? d - pulled : d);
+                }
+            if (!a.renormalize) shared = pulled;
+            wave_sync();
+        }
+        float high = -kInf;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) high = fmaxf(high, v[i]);   // not a NaN
+        high = group_max<G>(high);
+        const float inv = inverse(exps<G, PER>(v, p, high));
         float mean = 0.0f;
+        if (a.dloss) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = Row<G, PER>::at(i, g);
-            pull[i] = e < E ? a.pull[e] : 0.0f;
-            p[i] *= inv;
-            mean = __builtin_fmaf(p[i], pull[i], mean);
+            for (int i = 0; i < PER; ++i) mean = __builtin_fmaf(p[i], pull[i], mean);
+            mean = group_sum<G>(mean) * inv;
         }
-        mean = group_sum<G>(mean);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = p[i] * __builtin_fmaf(dloss, pull[i] - mean, -shared);
-    } else {
+        for (int i = 0; i < PER; ++i)
+            v[i] = p[i] * inv * __builtin_fmaf(dloss, pull[i] - mean, -shared);
+        if (a.dweights) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = p[i] * inv * -shared;
-    }
-    __syncthreads();
-    if (!inside) return;
-    if (a.dweights) {
+            for (int c = 0; c < PER / R::kRun; ++c) {
+                const Run x = *(const Run*)(extra + (c * G + g) * R::kRun);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = Row<G, PER>::at(i, g);
-            if (e < E) v[i] += extra[e];
+                for (int k = 0; k < R::kRun; ++k) {
+                    if constexpr (R::kRun == 1) v[c] += x[0];
+                    else v[c * R::kRun + k] += x[k];
+                }
+            }
+            wave_sync();   // the next token's go to the same places
         }
-    }
-    if (!live) {
+        if (!live) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+            for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+        }
+        if (inside) R::store(v, a.dlogits, t * E, E, g, a.wide);
     }
-    Row<G, PER>::store(v, a.dlogits, t * E, E, g, a.wide);
 }
 
 // ---- launches
 
 template <int G, int PER, bool LOSS>
 hipError_t choose(const RouteArgs& a, hipStream_t stream) {
-    // one pass over the tile if its lanes fit a workgroup, and the waves' sums of p 32 KiB
-    int threads = (int)min((int64_t)1024, ((int64_t)a.tile * G + 63) / 64 * 64);
+    // one tile: one pass over it if its lanes fit a workgroup; several: workgroups of 256, of
+    // which a CU holds more at once (65536 x 256 fp32: CHOOSE_A -> CHOOSE_B us).  The waves'
+    // sums of p stay within 32 KiB
+    int threads = (int)min((int64_t)(a.tiles == 1 ? kOneThreads : kTileThreads), ((int64_t)a.tile * G + 63) / 64 * 64);
     if (LOSS)
         while (threads > 64 && threads / 64 * a.E * 4 > 32768) threads = threads / 128 * 64;
     const int bytes = shared_of(a.E, a.top, a.tile, threads, LOSS).bytes;
@@ -670,29 +901,21 @@ hipError_t route(const RouteArgs& a, hipStream_t stream) {
         else e = choose<64, 16, LOSS>(a, stream);
     }
     if (e != hipSuccess || a.tiles == 1) return e;
+    if (a.tiles <= kJoined) {
+        place_kernel<LOSS, true><<<a.tiles + 1, kPlaceThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     sum_tiles_kernel<LOSS><<<a.E / kScanCols + 1, kScanCols * kScanRuns, 0, stream>>>(a);
-    const int64_t per = kPlaceThreads * kPlaceEach, slots = a.T * a.top;
-    const int64_t groups = slots > 0 ? (slots + per - 1) / per : 1;
-    place_kernel<LOSS><<<(unsigned)groups, kPlaceThreads, 0, stream>>>(a);
+    place_kernel<LOSS, false><<<a.tiles + 1, kPlaceThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <int G, int PER>
 hipError_t back(const BackArgs& a, hipStream_t stream) {
-    constexpr int64_t kPer = kBackThreads / G, kMost = 1 << 22;   // launches stay below 2^32 lanes
-    for (int64_t from = 0; from < a.T; from += kMost * kPer) {
-        BackArgs b = a;
-        const int64_t n = min(a.T - from, kMost * kPer);
-        b.T = n;
-        b.logits = (const uint8_t*)a.logits + from * a.ld * kBytes;
-        b.valid = a.valid ? a.valid + from : nullptr;
-        b.weights = a.weights + from * a.top;
-        b.experts = a.experts + from * a.top;
-        b.dweights = a.dweights ? a.dweights + from * a.top : nullptr;
-        b.dlogits = (uint8_t*)a.dlogits + from * a.E * kBytes;
-        back_kernel<G, PER><<<(unsigned)((n + kPer - 1) / kPer), kBackThreads,
-                              kBackThreads / G * a.E * 4, stream>>>(b);
-    }
+    // every workgroup takes several tokens in turn: pull is read once for them
+    constexpr int64_t kPer = kBackThreads / G, kMost = 2048;
+    const int64_t groups = min((a.T + kPer - 1) / kPer, kMost);
+    back_kernel<G, PER><<<(unsigned)groups, kBackThreads, kPer * G * PER * 4, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -40,10 +40,11 @@ bool stride_ok(int64_t ld, int64_t W, int64_t T) {
 
 int element_bytes(uint32_t type) { return type == ROUTE_FP32 ? 4 : 2; }
 
-// Tokens per tile (at most kTile): a workgroup's rounds and the tiles whose counts have
-// to be added up pull either way.
+// Tokens per tile (at most kTile, whole rounds of a workgroup of 256): few where it saves
+// the kernel that adds the tiles' counts up, else as many workgroups as fill the chip.
 int tile_of(int64_t T) {
-    if (T <= kTile) return kTile;
+    if (T <= kTile) return T > 0 ? (int)T : kTile;
+    if (T <= kTile * kJoined) return (int)((T + 16 * kJoined - 1) / (16 * kJoined)) * 16;
     return T <= 16384 ? 16 : T <= 32768 ? 32 : kTile;
 }
 

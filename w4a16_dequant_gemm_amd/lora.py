@@ -86,9 +86,12 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     if a.shape[2] != K or tuple(b.shape) != (L, N, R):
         _bad(f"{where}: a is {tuple(a.shape)}, b {tuple(b.shape)}, base {tuple(base.shape)}, "
              f"x {tuple(x.shape)}")
-    _require(a, f"{where}: a", dt, L * R * K, base.device)
-    _require(b, f"{where}: b", dt, L * N * R, base.device)
-    _require(ids, f"{where}: ids", torch.int32, M, base.device)
+    if not (a.dtype == b.dtype == dt and ids.dtype == torch.int32 and ids.numel() == M
+            and a.is_contiguous() and b.is_contiguous() and ids.is_contiguous()
+            and a.get_device() == b.get_device() == ids.get_device() == dev):
+        _require(a, f"{where}: a", dt, L * R * K, base.device)       # one of them raises with the
+        _require(b, f"{where}: b", dt, L * N * R, base.device)       # details
+        _require(ids, f"{where}: ids", torch.int32, M, base.device)
     if scale is not None:
         _require(scale, f"{where}: scale", torch.float32, L, base.device)
     if xs is not None:

@@ -104,12 +104,17 @@ def route_tokens(logits: torch.Tensor, top: int, renormalize: bool = True,
         _bad(f"{where}: top is {top}, there are {E} experts")
     dev, device = logits.get_device(), logits.device
     v = _valid_pointer(valid, where, T, device)
-    weights = _empty_on(stream, (T, top), torch.float32, device)
-    experts = _empty_on(stream, (T, top), torch.int32, device)
-    places = _empty_on(stream, (T, top), torch.int32, device)
-    rows = _empty_on(stream, (T * top,), torch.int32, device)
-    counts = _empty_on(stream, (E,), torch.int32, device)
-    offsets = _empty_on(stream, (E + 1,), torch.int32, device)
+    # one allocation for the outputs: offsets and rows, which the products read, 16-byte
+    # aligned (6 allocations take 10 us, one and its parts 7)
+    n, at_rows = T * top, (E + 4) // 4 * 4
+    whole = _empty_on(stream, (at_rows + 4 * n + E,), torch.int32, device)
+    shape, strides = (T, top), (top, 1)
+    offsets = whole.as_strided((E + 1,), (1,), 0)
+    rows = whole.as_strided((n,), (1,), at_rows)
+    experts = whole.as_strided(shape, strides, at_rows + n)
+    places = whole.as_strided(shape, strides, at_rows + 2 * n)
+    weights = whole.as_strided(shape, strides, at_rows + 3 * n).view(torch.float32)
+    counts = whole.as_strided((E,), (1,), at_rows + 4 * n)
     loss = _empty_on(stream, (), torch.float32, device) if balance else None
     pull = _empty_on(stream, (E,), torch.float32, device) if balance else None
     handle = _launch_stream(where, stream, dev)
