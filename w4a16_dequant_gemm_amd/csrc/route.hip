@@ -598,12 +598,12 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_ke
 }
 
 // Over the tiles, expert by expert (column E: the valid tokens): counts become the sum of
-// the tiles before, sums of p add up.  A workgroup takes 16 columns, 64 runs of tiles at
-// once; the runs' sums are added in their order.
-constexpr int kScanCols = 16, kScanRuns = 64, kScanEach = 16;
+// the tiles before, sums of p add up.  A workgroup takes 4 columns, 256 runs of up to 4 tiles
+// at once (1024 tiles of 256 experts: SCAN_US us, with 16 columns 9.0); the runs' sums
+// are added in their order.
+constexpr int kScanCols = 4, kScanRuns = 256, kScanEach = 4, kScanWaves = kScanCols * kScanRuns / 64;
 
-// Sums over the runs of the tiles that this and all threads of a column hold: a run is a
-// group of 16 lanes, 4 of them in a wave.
+// Sums over the runs of the tiles that this and all threads of a column hold.
 struct RunSums {
     int before, all;
 };
@@ -611,15 +611,16 @@ struct RunSums {
 __device__ __forceinline__ RunSums sum_runs(int mine, int (*part)[kScanCols]) {
     const int c = threadIdx.x % kScanCols, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int upto = mine;
-    int other = __shfl_up(upto, 16, 64);
-    if (lane >= 16) upto += other;
-    other = __shfl_up(upto, 32, 64);
-    if (lane >= 32) upto += other;
-    if (lane >= 48) part[wave][c] = upto;
+#pragma unroll
+    for (int off = kScanCols; off < 64; off <<= 1) {
+        const int other = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += other;
+    }
+    if (lane >= 64 - kScanCols) part[wave][c] = upto;
     __syncthreads();
     RunSums sum = {upto - mine, 0};
 #pragma unroll
-    for (int w = 0; w < kScanRuns / 4; ++w) {
+    for (int w = 0; w < kScanWaves; ++w) {
         const int p = part[w][c];
         if (w < wave) sum.before += p;
         sum.all += p;
@@ -628,25 +629,25 @@ __device__ __forceinline__ RunSums sum_runs(int mine, int (*part)[kScanCols]) {
     return sum;
 }
 
-// The same runs' floats, in their order; the result is for the threads of wave 0.
+// The same runs' floats, in a fixed order; the result is for the first wave.
 __device__ __forceinline__ float sum_runs(float mine, float (*part)[kScanCols]) {
     const int c = threadIdx.x % kScanCols, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    mine += __shfl_down(mine, 16, 64);
-    mine += __shfl_down(mine, 32, 64);
-    if (lane < 16) part[wave][c] = mine;
+#pragma unroll
+    for (int off = kScanCols; off < 64; off <<= 1) mine += __shfl_xor(mine, off, 64);
+    if (lane < kScanCols) part[wave][c] = mine;
     __syncthreads();
     float sum = 0.0f;
     if (wave == 0)
 #pragma unroll
-        for (int w = 0; w < kScanRuns / 4; ++w) sum += part[w][c];
+        for (int w = 0; w < kScanWaves; ++w) sum += part[w][c];
     __syncthreads();
     return sum;
 }
 
 template <bool LOSS>
 __global__ __launch_bounds__(kScanCols* kScanRuns) void sum_tiles_kernel(RouteArgs a) {
-    __shared__ int part[kScanRuns / 4][kScanCols];
-    __shared__ float part_p[kScanRuns / 4][kScanCols];
+    __shared__ int part[kScanWaves][kScanCols];
+    __shared__ float part_p[kScanWaves][kScanCols];
     const int c = threadIdx.x % kScanCols, run = threadIdx.x / kScanCols;
     const int e = blockIdx.x * kScanCols + c, E = a.E;
     int carry = 0;
