@@ -44,7 +44,8 @@ extern "C" {
 /* Workspace bytes lora_add needs (0 if the arguments are bad or M is 0).  It is laid out
  * like the workspaces of w4a16_gemm, whose counters it leaves as they are, and needs no
  * fill of its own. */
-size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, uint32_t flags);
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                            uint32_t flags);
 
 /*
  *   base   dev, [M] rows of N, ldb apart;

@@ -189,15 +189,18 @@ def test_lora_rejects_before_any_launch(lib):
 
 def test_lora_workspace(lib):
     size = lib.lora_workspace_bytes
-    assert size(0, 256, 512, 16, 0) == 0
-    assert size(4, 256, 512, 12, 0) == 0
-    assert size(4, 256, 512, 16, 0x40) == 0
-    for M, N, K, R in ((1, 1, 8, 8), (64, 28672, 8192, 16), (4096, 28672, 8192, 64),
-                       (100000, 64, 28672, 256)):
-        need = size(M, N, K, R, 0)
+    assert size(0, 256, 512, 16, 4, 0) == 0
+    assert size(4, 256, 512, 12, 4, 0) == 0
+    assert size(4, 256, 512, 16, 4, 0x40) == 0
+    assert size(4, 256, 512, 16, 0, 0) == 0
+    for M, N, K, R, L in ((1, 1, 8, 8, 1), (64, 28672, 8192, 16, 32), (4096, 28672, 8192, 64, 4),
+                          (300, 64, 512, 16, 64), (300, 64, 512, 16, 65),
+                          (100000, 64, 28672, 256, 1000)):
+        need = size(M, N, K, R, L, 0)
+        places = M + 64 * (min(L, 64) + 1)     # adapters' rows begin whole groups
         # parts of the first product, and for many rows operands and an order
-        assert 65536 + M * R * 4 <= need <= 65536 + M * (R * 64 + (R + 31) // 32 * 128 + 12)
-        assert size(M, N, K, R, 1) == need
+        assert 65536 + M * R * 4 <= need <= 65536 + places * (R * 64 + (R + 31) // 32 * 128 + 12)
+        assert size(M, N, K, R, L, 1) == need
 
 
 def test_binding_rejects_host_tensors(lib):

@@ -62,22 +62,30 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
                                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
 }
 
-// Rows are counted in the order of the calls' `order`, or as they are.
-__device__ __forceinline__ int64_t row_of(const LoraArgs& a, int64_t at) {
-    at = min(at, a.M - 1);
-    return a.order ? a.order[at] : at;
+// Rows have places: their own, or those of `order`, where a place may be empty (-1).
+__device__ __forceinline__ int row_or_none(const LoraArgs& a, int64_t at) {
+    if (at >= a.P) return -1;
+    return a.order ? a.order[at] : (int)at;
 }
 
-// The adapter of row `lane` of a group of `rows` rows from row0, -1 without one.
+// Some row to read for an empty place.
+__device__ __forceinline__ int64_t row_of(const LoraArgs& a, int64_t at) {
+    return max(row_or_none(a, at), 0);
+}
+
+// The adapter at place `lane` of a group of `rows` from row0, -1 without one.
 __device__ __forceinline__ int row_id(const LoraArgs& a, int64_t row0, int rows, int lane) {
     int id = -1;
-    if (lane < rows && row0 + lane < a.M) id = a.order ? a.sorted[row0 + lane] : a.ids[row0 + lane];
+    if (lane < rows && row0 + lane < a.P) id = a.order ? a.sorted[row0 + lane] : a.ids[row0 + lane];
     return id >= 0 && id < a.L ? id : -1;
 }
 
 // Rows by adapter, those without one last: a counting sort over the ids' remainders (a
-// group of rows may hold anything, so adapters that share a remainder only cost time).  One
-// workgroup: 4096 rows take SORT_US us.
+// group of rows may hold anything, so adapters that share a remainder only cost time).  With
+// few adapters each one's rows begin a group of their own (pad rows), the places before
+// it stay empty: no group does its work twice, which would keep a whole round of
+// workgroups waiting (4096 rows of 3 requests, K = 8192, N = 28672, R = 64: 158 -> PADDED_US
+// us).  One workgroup: 4096 rows take SORT_US us.
 constexpr int kBins = 1024;
 
 // Adds one for every live lane to its bin; returns what the lane found there.  Lanes of one
@@ -114,7 +122,8 @@ __global__ __launch_bounds__(1024) void sort_kernel(LoraArgs args) {
         count_up(first, bin(row < args.M ? args.ids[row] : -1), row < args.M);
     }
     __syncthreads();
-    const int mine = first[t];
+    const int count = first[t];
+    const int mine = args.pad ? (count + args.pad - 1) / args.pad * args.pad : count;
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -123,9 +132,14 @@ __global__ __launch_bounds__(1024) void sort_kernel(LoraArgs args) {
     }
     if ((t & 63) == 63) part[t >> 6] = upto;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < (t >> 6); ++w) before += part[w];
+    int before = 0, all = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < (t >> 6)) before += part[w];
+        all += part[w];
+    }
     first[t] = before + upto - mine;
+    for (int64_t at = first[t] + count; at < before + upto; ++at) args.order[at] = args.sorted[at] = -1;
+    for (int64_t at = all + t; at < args.P; at += 1024) args.order[at] = args.sorted[at] = -1;
     __syncthreads();
     auto put = [&](int64_t row, int id) {
         const int at = count_up(first, bin(id), row < args.M);
@@ -287,7 +301,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
             // a lane's numbers are 4 consecutive ranks of one row
             const int rank = rank0 + wave * 16 + g * 4;
             if ((same >> col & 1) && rank < args.R)
-                *(f32x4*)(args.h + ((int64_t)split * args.M + row0 + col) * args.R + rank) = sum;
+                *(f32x4*)(args.h + ((int64_t)split * args.P + row0 + col) * args.R + rank) = sum;
         }
         __syncthreads();
     }
@@ -343,7 +357,7 @@ __device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[K
         f32x4 p = {}, q = {};
         if (rank < args.R) {
             const float* h = args.h + row * args.R + rank;
-            const int64_t next = args.M * args.R;
+            const int64_t next = args.P * args.R;
             int s = 0;
             for (; s + 4 <= args.splits; s += 4) {
                 f32x4 a[4], c[4];
@@ -483,15 +497,15 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
     const int64_t first = part * args.up_each * kUpCols;
     const int64_t end = min(args.N, first + (int64_t)args.up_each * kUpCols);
     const int64_t whole = min(end, args.N / kUpCols * kUpCols);   // a run from here on ends inside
-    if (row0 >= args.M || first >= end) return;
+    if (row0 >= args.P || first >= end) return;
 
     const int id = row_id(args, row0, 16, lane);
-    const int own = (int)row_of(args, row0 + col);
+    const int own = row_or_none(args, row0 + col);
     unsigned long long todo = __ballot(id >= 0);
-    if (blockIdx.z == 0 && args.out != args.base && !(todo >> col & 1) && row0 + col < args.M) {
+    if (blockIdx.z == 0 && args.out != args.base && !(todo >> col & 1) && own >= 0) {
         // rows without an adapter
-        const uint16_t* from = (const uint16_t*)args.base + own * args.ldb;
-        uint16_t* to = (uint16_t*)args.out + own * args.ldo;
+        const uint16_t* from = (const uint16_t*)args.base + (int64_t)own * args.ldb;
+        uint16_t* to = (uint16_t*)args.out + (int64_t)own * args.ldo;
         for (int64_t n0 = first; n0 < end; n0 += kUpCols)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -705,7 +719,7 @@ __global__ __launch_bounds__(512, 2) void down_wide_kernel(LoraArgs args) {
 #pragma unroll
             for (int rg = 0; rg < RG; ++rg) {
                 const int rank = rank0 + rg * 16 + g * 4;
-                const int64_t row = (int64_t)split * args.M + row0 + tile * 16 + col;
+                const int64_t row = (int64_t)split * args.P + row0 + tile * 16 + col;
                 if (rank < args.R)
                     *(f32x4*)(args.h + row * args.R + rank) = acc[rg] + other[rg * 64 + lane];
             }
@@ -722,7 +736,7 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
     constexpr int kEach = (KH + 1) / 2;   // runs of 64 ranks, 4 per lane
     const int lane = threadIdx.x & 15;
     const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-    if (row >= args.M) return;
+    if (row >= args.P) return;
     const int id = args.order ? args.sorted[row] : args.ids[row];
     if (id < 0 || id >= args.L) return;
     const float scale = args.scale ? args.scale[id] : 1.0f;
@@ -739,11 +753,11 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
                 f32x4 p[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    p[k] = *(const f32x4*)(h + (s + k) * args.M * args.R);
+                    p[k] = *(const f32x4*)(h + (s + k) * args.P * args.R);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sum[i] += p[k];
             }
-            for (; s < args.splits; ++s) sum[i] += *(const f32x4*)(h + s * args.M * args.R);
+            for (; s < args.splits; ++s) sum[i] += *(const f32x4*)(h + s * args.P * args.R);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -805,8 +819,8 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = wave * 16 + g * 4 + j;
-            if ((todo >> r & 1) || row0 + r >= args.M) continue;
-            const int64_t row = row_of(args, row0 + r);
+            const int64_t row = row_or_none(args, row0 + r);
+            if ((todo >> r & 1) || row < 0) continue;
             const uint16_t* from = (const uint16_t*)args.base + row * args.ldb;
             uint16_t* to = (uint16_t*)args.out + row * args.ldo;
             for (int64_t n = mine0; n < end + col * 8; n += kWideCols) {
@@ -942,10 +956,10 @@ template <bool FP8, int RG>
 hipError_t down(const LoraArgs& a, hipStream_t stream) {
     const int slices = (a.R + 16 * RG - 1) / (16 * RG);
     if (a.many) {
-        const dim3 grid((unsigned)((a.M + 63) / 64), (unsigned)(a.splits * slices));
+        const dim3 grid((unsigned)((a.P + 63) / 64), (unsigned)(a.splits * slices));
         down_wide_kernel<FP8, RG><<<grid, 512, 0, stream>>>(a);
     } else {
-        const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)(a.splits * slices),
+        const dim3 grid((unsigned)((a.P + 15) / 16), (unsigned)(a.splits * slices),
                         (unsigned)a.down_z);
         down_kernel<FP8, RG><<<grid, kDownWaves * 64, 0, stream>>>(a);
     }
@@ -967,11 +981,11 @@ hipError_t up(const LoraArgs& a, hipStream_t stream) {
     if (a.many) {
         const int64_t cols = (int64_t)kWideCols * a.up_each;
         const int64_t blocks = (a.N + cols - 1) / cols;
-        join_kernel<KH><<<(unsigned)((a.M + 15) / 16), 256, 0, stream>>>(a);
-        up_wide_kernel<KH><<<(unsigned)((a.M + 63) / 64 * ((blocks + 7) / 8 * 8)), 256, 0, stream>>>(a);
+        join_kernel<KH><<<(unsigned)((a.P + 15) / 16), 256, 0, stream>>>(a);
+        up_wide_kernel<KH><<<(unsigned)((a.P + 63) / 64 * ((blocks + 7) / 8 * 8)), 256, 0, stream>>>(a);
     } else {
         const int64_t cols = (int64_t)kUpCols * (kUpWaves / a.up_wide) * a.up_each;
-        const dim3 grid((unsigned)((a.M + 16 * a.up_wide - 1) / (16 * a.up_wide)),
+        const dim3 grid((unsigned)((a.P + 16 * a.up_wide - 1) / (16 * a.up_wide)),
                         (unsigned)((a.N + cols - 1) / cols), (unsigned)a.up_z);
         up_kernel<KH><<<grid, kUpWaves * 64, 0, stream>>>(a);
     }

@@ -38,36 +38,52 @@ bool stride_ok(int64_t ld, int64_t W, int64_t M) {
 // The plan goes by the shape alone, so a row's sums are taken the same way whatever the
 // ids, and the workspace is known before the call.
 void set_plan(LoraArgs& a) {
-    const int steps = (int)ceil_div(a.K, kStep);
-    a.many = a.M >= 512;
-    a.by_adapter = a.M >= 128;
-    // first product: K in parts until there is a workgroup for every CU; where every wave of
-    // the second product adds the parts up itself, no more than pay for that
-    const int64_t tiles = ceil_div(a.M, a.many ? 64 : 16), slices = rank_slices(a.R);
-    a.splits = (int32_t)std::clamp<int64_t>(
-        a.many ? 256 / (tiles * slices) : std::max<int64_t>(16 / tiles, 4), 1,
-        std::min<int64_t>(ceil_div(steps, a.many ? 4 : kDownWaves), 16));
-    // adapters that a group of 16 rows may hold, in the mean if the rows are ordered
-    const int64_t most = std::min<int64_t>(
-        {a.L, a.M, 16, a.by_adapter ? 1 + ceil_div(16 * (int64_t)a.L, a.M) : 16});
-    a.down_z = (int32_t)std::clamp<int64_t>(1024 / (tiles * slices * a.splits), 1, most);
-    // second product
-    const int64_t runs = ceil_div(a.N, a.many ? 128 : kUpCols);
+    const int64_t steps = ceil_div(a.K, kStep), slices = rank_slices(a.R);
+    // The forms for many rows take 64 at a time.  Up to 32 ranks they pay from 1024 rows on
+    // (4 requests, K = 8192, N = 28672, R = 16: 512 rows 36 us either way, 1024 rows 51
+    // against 56), if they are not of too many adapters for that (1024 rows of 64 at
+    // random: 93 against 65); above from 512 (R = 64: 38 against 59).
+    a.many = a.R <= 32 ? a.M >= 1024 && a.M >= 32 * (int64_t)a.L : a.M >= 512;
+    a.by_adapter = a.M >= 128 && a.L > 1;
+    // groups of one adapter each; with more adapters than that, empty groups would cost more
+    // than the turns of mixed ones
+    const int64_t group = a.many ? 64 : 16;
+    a.pad = a.by_adapter && a.L <= 64 ? (int32_t)group : 0;
+    a.P = a.pad ? (a.M / group + a.L + 1) * group : a.M;
     if (a.many) {
-        // runs of columns per workgroup: few rounds of the workgroups that the chip holds at
-        // once (two per CU up to 96 ranks), of which each costs three runs besides its own
-        const int64_t held = a.R <= 96 ? 512 : 256;
+        // groups that hold a row: half of the adapters' last ones on top
+        const int64_t tiles = ceil_div(a.M, 64) + (a.pad ? a.L / 2 : 0);
+        // First product: few rounds of the workgroups that the chip holds at once, each of
+        // which costs its pairs of steps and about 6 more.
         int64_t best = 0;
-        for (int64_t each = 1; each <= 16; ++each) {
-            const int64_t rounds = ceil_div(tiles * ceil_div(runs, each), held);
-            if (best == 0 || rounds * (each + 3) < best) {
-                best = rounds * (each + 3);
-                a.up_each = (int32_t)each;
-            }
+        for (int64_t splits = 1; splits <= std::min<int64_t>(16, ceil_div(steps, 4)); ++splits) {
+            const int64_t cost =
+                ceil_div(tiles * slices * splits, 256) * (ceil_div(steps, 2 * splits) + 6);
+            if (best == 0 || cost < best) best = cost, a.splits = (int32_t)splits;
         }
-        a.up_z = a.up_wide = 1;
+        // Second product: a workgroup's time is its runs of columns and one and a half more;
+        // all of them over the places there are, the 8 XCDs with as many blocks of columns
+        // each, and half of one at the end.
+        const int64_t runs = ceil_div(a.N, 128), held = a.R <= 96 ? 512 : 256;
+        double least = 0.0;
+        for (int64_t each = 1; each <= 16; ++each) {
+            const int64_t groups = tiles * ceil_div(ceil_div(runs, each), 8) * 8;
+            const double one = (double)each + 1.5;
+            const double cost = std::max(one, one * (double)groups / (double)held) + 0.5 * one;
+            if (least == 0.0 || cost < least) least = cost, a.up_each = (int32_t)each;
+        }
+        a.down_z = a.up_z = a.up_wide = 1;
         return;
     }
+    const int64_t tiles = ceil_div(a.M, 16), runs = ceil_div(a.N, kUpCols);
+    // adapters that a group may hold, in the mean if the rows are ordered
+    const int64_t mean = a.by_adapter ? 1 + ceil_div(16 * (int64_t)a.L, a.M) : 16;
+    const int64_t most = a.pad ? 1 : std::min<int64_t>({a.L, a.M, 16, mean});
+    // first product: K in parts until there is a workgroup for every CU, but no more than pay
+    // for every wave of the second product adding the parts up itself
+    a.splits = (int32_t)std::clamp<int64_t>(std::max<int64_t>(16 / tiles, 4), 1,
+                                            std::min<int64_t>(ceil_div(steps, kDownWaves), 16));
+    a.down_z = (int32_t)std::clamp<int64_t>(1024 / (tiles * slices * a.splits), 1, most);
     a.up_wide = tiles >= 8 ? 4 : 1;
     a.up_each = (int32_t)std::clamp<int64_t>(tiles * runs / 448, 1, 4);
     if (a.N >= (int64_t)1 << 23) a.up_each = 4;   // the grid's second dimension stays below 2^16
@@ -82,10 +98,10 @@ struct Scratch {
 
 Scratch scratch_of(const LoraArgs& a) {
     Scratch s;
-    s.operands = a.splits * a.M * a.R * 4;
-    s.back = s.operands + (a.many ? a.M * ceil_div(a.R, 32) * 128 : 0);
-    s.order = s.back + (a.many ? a.M * 4 : 0);
-    s.bytes = kSkip + s.order + (a.by_adapter ? a.M * 8 : 0);
+    s.operands = a.splits * a.P * a.R * 4;
+    s.back = s.operands + (a.many ? a.P * ceil_div(a.R, 32) * 128 : 0);
+    s.order = s.back + (a.many ? a.P * 4 : 0);
+    s.bytes = kSkip + s.order + (a.by_adapter ? a.P * 8 : 0);
     return s;
 }
 
@@ -97,10 +113,11 @@ using namespace lora;
 
 extern "C" {
 
-size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, uint32_t flags) {
-    if (check_shape(M, N, K, R, flags) != W4A16_OK || M == 0) return 0;
+size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                            uint32_t flags) {
+    if (check_shape(M, N, K, R, flags) != W4A16_OK || M == 0 || L < 1 || L >= kMaxDim) return 0;
     LoraArgs a{};
-    a.M = M, a.N = N, a.K = K, a.R = (int32_t)R, a.L = 1;
+    a.M = M, a.N = N, a.K = K, a.R = (int32_t)R, a.L = (int32_t)L;
     set_plan(a);
     return (size_t)scratch_of(a).bytes;
 }
@@ -135,9 +152,9 @@ w4a16_status_t lora_add(const void* base, int64_t ldb, const void* x, int64_t ld
     a.h = (float*)scratch;
     a.operands = (uint16_t*)(scratch + need.operands);
     a.back = (float*)(scratch + need.back);
-    if (a.by_adapter && L > 1) {
+    if (a.by_adapter) {
         a.order = (int32_t*)(scratch + need.order);
-        a.sorted = a.order + M;
+        a.sorted = a.order + a.P;
     }
     return from_hip(flags & LORA_BF16 ? launch_bf16(a, fp8, (hipStream_t)stream)
                                       : launch_f16(a, fp8, (hipStream_t)stream));

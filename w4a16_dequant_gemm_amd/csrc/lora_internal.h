@@ -24,14 +24,16 @@ struct LoraArgs {
     const float* scale;   // may be null
     const int32_t* ids;
     void* out;
-    int32_t* order;       // [M] rows by adapter (null: as they are), and their ids
+    int32_t* order;       // [P] rows by adapter (null: as they are), and their ids
     int32_t* sorted;
-    float* h;             // [splits][M][R]: partial inner products with A
-    // many rows: operands of the second product, [M][2][R filled up to 32], and (fp16) what
+    float* h;             // [splits][P][R]: partial inner products with A
+    // many rows: operands of the second product, [P][2][R filled up to 32], and (fp16) what
     // a row's products are multiplied by
     uint16_t* operands;
     float* back;
     int64_t ldb, ldx, ldo, M, N, K;
+    int64_t P;            // places of rows
+    int32_t pad;          // each adapter's rows begin at a multiple of it (0: anywhere)
     int32_t R, L, KB;     // KB: fp8 scales per row
     int32_t many;         // the forms for many rows
     int32_t by_adapter;   // order the rows first

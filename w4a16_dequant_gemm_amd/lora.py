@@ -29,7 +29,7 @@ def _lib():
     if _declared is None:
         lib = load_library()
         p, i64, u32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
-        lib.lora_workspace_bytes.argtypes = [i64, i64, i64, i64, u32]
+        lib.lora_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, u32]
         lib.lora_workspace_bytes.restype = sz
         lib.lora_add.argtypes = [p, i64, p, i64, p, p, p, p, p, p, i64, i64, i64, i64, i64, i64, u32,
                                  p, sz, p]
@@ -38,8 +38,8 @@ def _lib():
     return _declared
 
 
-def lora_workspace_bytes(M: int, N: int, K: int, R: int, flags: int) -> int:
-    return int(_lib().lora_workspace_bytes(M, N, K, R, flags))
+def lora_workspace_bytes(M: int, N: int, K: int, R: int, L: int, flags: int) -> int:
+    return int(_lib().lora_workspace_bytes(M, N, K, R, L, flags))
 
 
 def _rows(t: torch.Tensor, where: str, name: str, dtypes) -> int:
@@ -108,10 +108,10 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
             _bad(f"{where}: out is {tuple(out.shape)} on {out.device}")
     handle = _launch_stream(where, stream, dev)
     if workspace is None:
-        key = (M, N, K, R, flags)
+        key = (M, N, K, R, L, flags)
         need = _ws_bytes.get(key)
         if need is None:
-            need = _keep_bytes(_ws_bytes, key, lora_workspace_bytes(M, N, K, R, flags))
+            need = _keep_bytes(_ws_bytes, key, lora_workspace_bytes(M, N, K, R, L, flags))
         if need:
             workspace = _scratch(need, base.device, stream, handle)
     else:
