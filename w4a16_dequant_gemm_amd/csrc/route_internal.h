@@ -10,7 +10,7 @@
 namespace route {
 
 constexpr int kTile = 64;          // tokens of a workgroup at most: one bit each in a 64-bit mask
-constexpr int kJoined = 64;        // tiles whose counts are not added up by a kernel of their own
+constexpr int kJoined = 64;       // tiles whose counts are not added up by a kernel of their own
 constexpr int64_t kSkip = 65536;   // the workspace's first bytes hold the products' counters
 
 struct RouteArgs {
