@@ -259,6 +259,7 @@ def bound(monkeypatch):
     monkeypatch.setattr(w4, "_stream_handle", lambda stream: 0)
     monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None:
                         Buffer(*((shape,) if isinstance(shape, int) else shape), dtype=dtype))
+    monkeypatch.setattr(torch, "empty_like", lambda like: FakeTensor(*like.shape, dtype=like.dtype))
     return route, lora
 
 

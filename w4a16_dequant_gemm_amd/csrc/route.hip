@@ -712,6 +712,7 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
     }
     // over all tiles, and over those before this one; column E: valid tokens
     int all[kPlaceCols], before[kPlaceCols];
+    float sums[LOSS ? kPlaceCols : 1];
 #pragma unroll
     for (int c = 0; c < kPlaceCols; ++c) {
         const int e = threadIdx.x + c * kPlaceThreads;
@@ -734,9 +735,32 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
             if (!totals && e < E) before[c] = a.tile_counts[(int64_t)tile * (E + 1) + e];
         }
         base[e] = all[c];
+        if constexpr (LOSS) {
+            sums[c] = 0.0f;
+            if (!totals || e == E) continue;
+            if constexpr (!JOIN) sums[c] = a.all_p[e];
+            for (int b0 = 0; JOIN && b0 < a.tiles; b0 += 16) {
+                float p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    p[i] = b0 + i < a.tiles ? a.tile_p[(b0 + i) * E + e] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sums[c] += p[i];
+            }
+        }
     }
     __syncthreads();
-    const int V = base[E];
+    if (LOSS && totals) {
+        finish_loss(a, base[E], (float*)part, [&](int e) { return base[e]; },
+                    [&](int e) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < kPlaceCols; ++c)
+                            sum = e == (int)threadIdx.x + c * kPlaceThreads ? sums[c] : sum;
+                        return sum;
+                    });
+        __syncthreads();
+    }
     const int total = scan_counts(base, E, part);
     if (totals) {
 #pragma unroll
@@ -748,22 +772,6 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
             }
         }
         if (threadIdx.x == 0) a.offsets[E] = total;
-        if constexpr (LOSS)
-            finish_loss(a, V, (float*)part,
-                        [&](int e) { return (e + 1 < E ? base[e + 1] : total) - base[e]; },
-                        [&](int e) {
-                            if constexpr (!JOIN) return a.all_p[e];
-                            float sum = 0.0f;
-                            for (int b0 = 0; b0 < a.tiles; b0 += 16) {
-                                float p[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    p[i] = b0 + i < a.tiles ? a.tile_p[(b0 + i) * E + e] : 0.0f;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) sum += p[i];
-                            }
-                            return sum;
-                        });
         return;
     }
 #pragma unroll

@@ -100,7 +100,9 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
         if xs.dim() > 1 and xs.size(-1) != kb:
             _bad(f"{where}: xs is {tuple(xs.shape)}, its rows must hold {kb} scales")
     if out is None:
-        out = _empty_on(stream, (M, N), dt, base.device)
+        # empty_like: 1.2 us where empty with a shape and a device takes 1.7
+        out = (torch.empty_like(base) if stream is None and base.is_contiguous()
+               else _empty_on(stream, (M, N), dt, base.device))
         ldo = N
     else:
         ldo = _rows(out, where, "out", (dt,))

@@ -80,6 +80,13 @@ def _rows(t: torch.Tensor, where: str, name: str, dtypes) -> int:
     return ld
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """An output of t's shape and dtype, contiguous."""
+    # empty_like: 1.2 us where empty with a shape and a device takes 1.7
+    return (torch.empty_like(t) if stream is None and t.is_contiguous()
+            else _empty_on(stream, tuple(t.shape), t.dtype, t.device))
+
+
 def _valid_pointer(valid, where: str, T: int, device):
     if valid is None:
         return None
@@ -159,7 +166,7 @@ def route_tokens_backward(logits: torch.Tensor, routing: Routing,
     if dloss is not None:
         _require(dloss, f"{where}: dloss", torch.float32, 1, device)
         _require(routing.pull, f"{where}: pull (of a call with balance)", torch.float32, E, device)
-    dlogits = _empty_on(stream, (T, E), logits.dtype, device)
+    dlogits = _like(logits, stream)
     flags = _TYPES[logits.dtype] | (_RENORMALIZE if routing.renormalize else 0)
     _check(_lib().route_tokens_backward(
         logits.data_ptr(), ld, v, routing.weights.data_ptr(), routing.experts.data_ptr(),
@@ -200,7 +207,8 @@ def combine_rows(y: torch.Tensor, weights: torch.Tensor, places: torch.Tensor,
         if tuple(residual.shape) != (T, N) or residual.get_device() != y.get_device():
             _bad(f"{where}: residual is {tuple(residual.shape)} on {residual.device}")
     if out is None:
-        out = _empty_on(stream, (T, N), y.dtype, device)
+        out = (_like(residual, stream) if residual is not None
+               else _empty_on(stream, (T, N), y.dtype, device))
     else:
         _require(out, f"{where}: out", y.dtype, T * N, device)
     _check(_lib().route_combine(y.data_ptr(), ldy, weights.data_ptr(), places.data_ptr(),
@@ -229,8 +237,7 @@ def combine_rows_backward(dout: torch.Tensor, y: torch.Tensor, weights: torch.Te
     _require(offsets, f"{where}: offsets", torch.int32, offsets.numel(), device)
     if offsets.numel() < 1 or R > T * top:
         _bad(f"{where}: {R} rows for {T} tokens of {top} slots, {offsets.numel()} offsets")
-    dy = _empty_on(stream, (R, N), y.dtype, device)
-    dweights = _empty_on(stream, (T, top), torch.float32, device)
+    dy, dweights = _like(y, stream), _like(weights, stream)
     _check(_lib().route_combine_backward(dout.data_ptr(), ldd, y.data_ptr(), ldy,
                                          weights.data_ptr(), places.data_ptr(),
                                          offsets.data_ptr() + 4 * (offsets.numel() - 1),
