@@ -11,7 +11,7 @@
  * seen in that adapter's or row's outputs only.  The R inner products with A are kept in
  * fp32; as operand of the second product each is split into two numbers of the
  * activations' type (fp16: after a row's were brought near 2^14 by a power of two), which
- * keeps 16 (bf16) or 22 (fp16) of its bits.  Sums have a fixed order: equal calls
+ * keeps 17 (bf16) or 22 (fp16) of its bits.  Sums have a fixed order: equal calls
  * give equal bits, and a row's result does not depend on the other rows' ids.
  *
  * Conventions are those of w4a16.h (plain C types, caller-owned device pointers, stream
