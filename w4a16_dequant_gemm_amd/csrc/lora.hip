@@ -534,7 +534,10 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
         // of its rows reads, so that no load has a condition
         const bool mine = same >> col & 1;
         const int64_t row = row0 + (mine ? col : one_row);
-        const int64_t actual = mine ? own : __builtin_amdgcn_readlane(own, one_row);
+        // read by every lane, outside the choice: a lane that is read must be active itself
+        // (inside, the copy of own that is read may have been made by the other lanes alone)
+        const int one_own = __builtin_amdgcn_readlane(own, one_row);
+        const int64_t actual = mine ? own : one_own;
         const uint16_t* base = (const uint16_t*)args.base + actual * args.ldb;
         uint16_t* out = (uint16_t*)args.out + actual * args.ldo;
         const uint16_t* b = (const uint16_t*)args.b + (int64_t)adapter * args.N * args.R;
