@@ -3,9 +3,8 @@
 //
 // Both are bound by HBM: every row of y is read once, nothing but the result is written
 // (bf16: 8192 tokens of 2 rows of 8192 with the residual 87 us, 6.1 TB/s; the gradient of
-// 8192 tokens of 8 rows of 4096 214 us, 5.3 TB/s; a device copy reaches 5.16).
-// A lane holds 8 consecutive elements of a token (one 16-byte access per row); a token's
-// places and weights are the same for the whole workgroup and come through scalar loads.
+// 8192 tokens of 8 rows of 4096 212 us, 5.3 TB/s; a device copy reaches 5.16).
+// A lane holds 8 consecutive elements of a token (one 16-byte access per row).
 // Rows may start at any element (an odd N): global memory takes 16-byte accesses at any
 // even address (the gradient of 519 tokens of 6 rows of 2831 takes 19.7 us, of 2832 17.4).
 #include <hip/hip_runtime.h>
@@ -40,7 +39,8 @@ __device__ __forceinline__ float element(u32x4 q, int i) {
 }
 
 // A lane's 8 columns.  The last lane of a row of N >= 8 takes its last 8, of which the
-// first `skip` are the lane's before it: loads need no condition.  SHORT: N < 8, one lane.
+// first `skip` are the lane's before it, lanes behind it have none of their own: loads need
+// no condition.  SHORT: N < 8.
 struct Columns {
     int64_t n;
     int skip;
@@ -48,7 +48,7 @@ struct Columns {
 
 template <bool SHORT>
 __device__ __forceinline__ Columns columns(int64_t first, int64_t N) {
-    if (SHORT) return {0, 0};
+    if (SHORT) return {0, (int)first};
     const int64_t n = min(first, N - kPiece);
     return {n, (int)(first - n)};
 }
@@ -79,33 +79,67 @@ __device__ __forceinline__ void store8(uint16_t* row, Columns c, int64_t N,
     }
 }
 
+// A token's slots from j0 on, one in each of the wave's lanes: two loads, where a load per
+// slot would wait for the one before it (8 tokens of 8 rows of 4096 3.9 -> 3.4 us, the
+// gradient of 519 tokens of 6 rows of 2831 19.4 -> 18.3).  Every lane of the wave is active.
+struct Slots {
+    int my_place, my_weight;
+
+    __device__ __forceinline__ int place(int j) const {   // none: -1
+        return __builtin_amdgcn_readlane(my_place, j);
+    }
+    __device__ __forceinline__ float weight(int j) const {
+        return __int_as_float(__builtin_amdgcn_readlane(my_weight, j));
+    }
+};
+
+__device__ __forceinline__ Slots slots_of(const CombineArgs& a, int64_t t, int j0, int lane,
+                                          int64_t rows) {
+    const int64_t at = t * a.top + min(j0 + lane, a.top - 1);
+    const int place = a.places[at];
+    return {j0 + lane < a.top && place >= 0 && place < rows ? place : -1,
+            __float_as_int(a.weights[at])};
+}
+
 // Workgroup (token, run of columns).  The rows of up to JG slots are in flight at once.
 template <bool BF16, int JG, bool SHORT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
     const int64_t t = a.first + blockIdx.x;
+    const int lane = threadIdx.x & 63;
     const int64_t first = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * kPiece;
-    if (first >= a.N) return;
+    if (first - lane * kPiece >= a.N) return;   // the whole wave: its lanes hold the slots
     const Columns c = columns<SHORT>(first, a.N);
-    const float* weights = a.weights + t * a.top;
-    const int32_t* places = a.places + t * a.top;
     float acc[kPiece];
     u32x4 r = {0u, 0u, 0u, 0u};
+    asm("" : "+v"(r));   // no constants: they would be widened, and r waited for, where it is read
     if (a.extra) r = load8<SHORT>((const uint16_t*)a.extra + t * a.lde, c.n, a.N);
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) acc[i] = element<BF16>(r, i);
     for (int j0 = 0; j0 < a.top; j0 += JG) {
+        const Slots slots = slots_of(a, t, j0, lane, a.R);
         u32x4 q[JG];
-        bool there[JG];
+        int64_t place[JG];
+        bool all = true;
 #pragma unroll
         for (int j = 0; j < JG; ++j) {
-            const int64_t p = j0 + j < a.top ? places[j0 + j] : -1;
-            there[j] = p >= 0 && p < a.R;
-            if (there[j]) q[j] = load8<SHORT>((const uint16_t*)a.y + p * a.ldy, c.n, a.N);
+            place[j] = slots.place(j);
+            all = all && place[j] >= 0;
         }
+        const uint16_t* y = (const uint16_t*)a.y;
+        // behind a condition, a load waits for those before it
+        if (all) {
+#pragma unroll
+            for (int j = 0; j < JG; ++j) q[j] = load8<SHORT>(y + place[j] * a.ldy, c.n, a.N);
+        } else {
+#pragma unroll
+            for (int j = 0; j < JG; ++j)
+                if (place[j] >= 0) q[j] = load8<SHORT>(y + place[j] * a.ldy, c.n, a.N);
+        }
+        if (j0 == 0)
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) acc[i] = element<BF16>(r, i);
 #pragma unroll
         for (int j = 0; j < JG; ++j) {
-            if (!there[j]) continue;
-            const float w = weights[j0 + j];
+            if (place[j] < 0) continue;
+            const float w = slots.weight(j);
 #pragma unroll
             for (int i = 0; i < kPiece; ++i)
                 acc[i] = __builtin_fmaf(w, element<BF16>(q[j], i), acc[i]);
@@ -119,19 +153,18 @@ template <bool BF16, int JG, bool SHORT>
 __global__ __launch_bounds__(kBackThreads) void combine_backward_kernel(CombineArgs a) {
     __shared__ float part[kBackThreads / 64][JG];
     const int64_t t = a.first + blockIdx.x;
-    const float* weights = a.weights + t * a.top;
-    const int32_t* places = a.places + t * a.top;
     const uint16_t* dout = (const uint16_t*)a.extra + t * a.lde;
     const int64_t routed = a.routed ? min((int64_t)max(*a.routed, 0), a.R) : a.R;
     const int64_t stride = (int64_t)blockDim.x * kPiece;
+    const int lane = threadIdx.x & 63;
     for (int j0 = 0; j0 < a.top; j0 += JG) {
+        const Slots slots = slots_of(a, t, j0, lane, routed);
         int64_t place[JG];
         float w[JG], dot[JG];
 #pragma unroll
         for (int j = 0; j < JG; ++j) {
-            place[j] = j0 + j < a.top ? places[j0 + j] : -1;
-            if (place[j] >= routed) place[j] = -1;
-            w[j] = place[j] >= 0 ? weights[j0 + j] : 0.0f;
+            place[j] = slots.place(j);
+            w[j] = slots.weight(j);
             dot[j] = 0.0f;
         }
         for (int64_t first = (int64_t)threadIdx.x * kPiece; first < a.N; first += stride) {
