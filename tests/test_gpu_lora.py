@@ -128,6 +128,15 @@ def test_lora(M, N, K, R, L, dtype, rows):
     check(lr().lora_add(**p), p, dtype)
 
 
+# every number of rank operands, with columns of the matrix instruction that hold no row
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("R", [24, 40, 96, 112, 144, 168, 192, 224, 248])
+def test_ranks_of_few_rows(R, dtype):
+    for how in ("one", "mixed"):
+        p = problem(9, 333, 256, R, 2, dtype, "x16", how)
+        check(lr().lora_add(**p), p, dtype)
+
+
 @pytest.mark.parametrize("K", [8, 24, 136, 1032])
 def test_widths_of_8(K):
     say(f"K={K}")
@@ -268,6 +277,24 @@ def test_offsets_beyond_32_bits():
                         torch.ones(2, 16, dtype=torch.bfloat16, device="cuda"), a, b,
                         torch.tensor([L - 1, L - 2], dtype=torch.int32, device="cuda"))
     assert float(out[0, -1]) == 16.0 and int(out.count_nonzero()) == 1
+
+
+# the most columns there may be: the grid's second dimension is at its largest
+@pytest.mark.parametrize("M", [1, 128])
+def test_most_columns(M):
+    N, K, R = (1 << 24) - 1, 16, 8
+    g = torch.Generator("cuda").manual_seed(M)
+    p = dict(base=torch.randn(M, N, generator=g, device="cuda", dtype=torch.bfloat16),
+             x=torch.randn(M, K, generator=g, device="cuda").bfloat16(),
+             a=torch.randn(1, R, K, generator=g, device="cuda").bfloat16(),
+             b=torch.randn(1, N, R, generator=g, device="cuda").bfloat16(),
+             ids=torch.zeros(M, dtype=torch.int32, device="cuda"), scale=None, xs=None)
+    p["ids"][3::7] = -1
+    got = lr().lora_add(**p)
+    for first in (0, N // 2 - 7, (N // 4096) * 4096 - 600, N - 1000):
+        n = slice(first, first + 1000)
+        part = dict(p, base=p["base"][:, n].contiguous(), b=p["b"][:, n].contiguous())
+        check(got[:, n].contiguous(), part, "bf16")
 
 
 def test_on_another_stream():

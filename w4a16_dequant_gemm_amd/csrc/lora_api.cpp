@@ -86,7 +86,7 @@ void set_plan(LoraArgs& a) {
     a.down_z = (int32_t)std::clamp<int64_t>(1024 / (tiles * slices * a.splits), 1, most);
     a.up_wide = tiles >= 8 ? 4 : 1;
     a.up_each = (int32_t)std::clamp<int64_t>(tiles * runs / 448, 1, 4);
-    if (a.N >= (int64_t)1 << 23) a.up_each = 4;   // the grid's second dimension stays below 2^16
+    if (a.N >= (int64_t)1 << 23) a.up_each = 8;   // the grid's second dimension stays below 2^16
     const int64_t waves = tiles * ceil_div(runs, a.up_each);
     a.up_z = (int32_t)std::clamp<int64_t>(8192 / waves, 1, most);
 }
