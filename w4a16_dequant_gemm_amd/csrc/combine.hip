@@ -6,7 +6,7 @@
 // 8192 tokens of 8 rows of 4096 212 us, 5.3 TB/s; a device copy reaches 5.16).
 // A lane holds 8 consecutive elements of a token (one 16-byte access per row).
 // Rows may start at any element (an odd N): global memory takes 16-byte accesses at any
-// even address (the gradient of 519 tokens of 6 rows of 2831 takes 19.7 us, of 2832 17.4).
+// even address (the gradient of 519 tokens of 6 rows of 2831 takes 14.0 us, of 2832 13.0).
 #include <hip/hip_runtime.h>
 
 #include "route_internal.h"
@@ -81,7 +81,8 @@ __device__ __forceinline__ void store8(uint16_t* row, Columns c, int64_t N,
 
 // A token's slots from j0 on, one in each of the wave's lanes: two loads, where a load per
 // slot would wait for the one before it (8 tokens of 8 rows of 4096 3.9 -> 3.4 us, the
-// gradient of 519 tokens of 6 rows of 2831 19.4 -> 18.3).  Every lane of the wave is active.
+// gradient of 519 tokens of 6 rows of 2831 in workgroups of 512 19.4 -> 18.3).  Every lane
+// of the wave is active.
 struct Slots {
     int my_place, my_weight;
 
@@ -244,7 +245,10 @@ hipError_t combine(CombineArgs a, hipStream_t stream) {
 
 template <bool BF16, int JG>
 hipError_t combine_backward(CombineArgs a, hipStream_t stream) {
-    const int threads = split_of(a.N, kBackThreads).threads;
+    // Few tokens: smaller workgroups, which the CUs share more evenly (519 tokens of 6 rows of
+    // 2831: 17.5 -> 14.0 us; 1024 of 2 of 8192: 17.7 -> 16.7).  Many: a row in one piece
+    // (4096 of 2 of 8192 56.2 against 56.9, 8192 of 8 of 4096 213 against 216).
+    const int threads = split_of(a.N, a.T <= 2048 ? kBackThreads / 2 : kBackThreads).threads;
     for (a.first = 0; a.first < a.T; a.first += kMostGroups) {
         const unsigned groups = (unsigned)min(a.T - a.first, kMostGroups);
         if (a.N < kPiece)
