@@ -844,13 +844,13 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
     }
     if (todo == 0) return;
 
-    // Where the pieces of a run go: piece q is 8 ranks of column q / (R / 8); pieces of
-    // ranks behind R stay zeros.
+    // Where the pieces of a run go: piece q is 8 ranks of column q / (R / 8), threads behind
+    // the last piece take that one too; pieces of ranks behind R stay zeros.
     const int per_col = args.R / 8, pieces = kWideCols * per_col;
     int place[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int q = threadIdx.x + i * 256, n = q / per_col;
+        const int q = min((int)threadIdx.x + i * 256, pieces - 1), n = q / per_col;
         place[i] = (n % 8 * 16 + n / 8) * kRowPitch + q % per_col * 16;
     }
     if (args.R % 32) {
@@ -864,19 +864,20 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
         const unsigned long long same = __ballot(id == adapter);
         todo &= ~same;
         const uint32_t tile_rows = (uint32_t)(same >> (wave * 16)) & 0xFFFFu;
-        const bool wanted = tile_rows != 0;   // the same for the wave
-        const int one_row = wanted ? __builtin_ctz(tile_rows) : 0;
+        // a row of the adapter; a tile without one works on any and stores nothing, since a
+        // load behind a condition would wait for those before it
+        const int one_row = tile_rows ? __builtin_ctz(tile_rows) : 0;
 
         const uint16_t* b = (const uint16_t*)args.b + (int64_t)adapter * args.N * args.R;
-        u32x4 w[kLoads], y[kWideRing][4];
-        auto load_adapter = [&](int64_t n0) {
+        auto load_adapter = [&](u32x4 (&w)[kLoads], int64_t n0, int last) {
             const uint8_t* run = (const uint8_t*)(b + n0 * args.R);
-            const int64_t left = (args.N - n0) * per_col;   // pieces of the columns inside N
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int q = threadIdx.x + i * 256;
-                if (q < pieces && q < left) w[i] = *(const u32x4*)(run + q * 16);
-            }
+            for (int i = 0; i < kLoads; ++i)
+                w[i] = *(const u32x4*)(run + min((int)threadIdx.x + i * 256, last) * 16);
+        };
+        auto keep_adapter = [&](uint8_t* my_ranks, const u32x4 (&w)[kLoads]) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) *(u32x4*)(my_ranks + place[i]) = w[i];
         };
         const uint16_t* base[4];
         uint16_t* out[4];
@@ -886,23 +887,13 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // other rows read what one of the adapter's reads
             const int64_t row = row_of(args, tile0 + (mine[j] ? g * 4 + j : one_row));
-            base[j] = (const uint16_t*)args.base + row * args.ldb + mine0;
-            out[j] = (uint16_t*)args.out + row * args.ldo + mine0;
+            base[j] = (const uint16_t*)args.base + row * args.ldb;
+            out[j] = (uint16_t*)args.out + row * args.ldo;
         }
-        auto load_base_run = [&](u32x4 (&r)[4], int64_t n0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                r[j] = __builtin_nontemporal_load((const u32x4_any*)(base[j] + (n0 - first)));
-        };
-        load_adapter(first);
         u32x4 high[KH], low[KH];
         float back[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if (wanted) {
-#pragma unroll
-            for (int j = 0; j < kWideRing; ++j)
-                if (first + j * kWideCols < whole)
-                    load_base_run(y[j], first + j * kWideCols);
-            const int64_t row = tile0 + (tile_rows >> col & 1 ? col : one_row);
+        {
+            const int64_t row = min(tile0 + (tile_rows >> col & 1 ? col : one_row), args.P - 1);
             const uint16_t* h = args.operands + row * (KH * 64) + g * 8;
 #pragma unroll
             for (int kh = 0; kh < KH; ++kh) {
@@ -911,52 +902,76 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
             }
             if constexpr (!BF16)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) back[j] = args.back[tile0 + (mine[j] ? g * 4 + j : one_row)];
+                for (int j = 0; j < 4; ++j)
+                    back[j] = args.back[min(tile0 + (mine[j] ? g * 4 + j : one_row), args.P - 1)];
         }
-        for (int64_t n0 = first; n0 < end;) {
+        auto multiply = [&](f32x4 (&d)[8], const uint8_t* my_ranks) {
+#pragma unroll
+            for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const u32x4 q = *(const u32x4*)(my_ranks + (t * 16 + col) * kRowPitch +
+                                                    (kh * 4 + g) * 16);
+                    d[t] = mfma(high[kh], q, d[t]);
+                    d[t] = mfma(low[kh], q, d[t]);
+                }
+        };
+        auto added = [&](u32x4 q, const f32x4 (&d)[8], int r) {
+            return add8(q, f32x4{d[0][r], d[1][r], d[2][r], d[3][r]},
+                        f32x4{d[4][r], d[5][r], d[6][r], d[7][r]}, back[r]);
+        };
+        if (first < whole) {
+            // runs behind the last one's are read too (the adapter's last, a piece of h for
+            // base), so that every load and its place in the order are known
+            const int64_t last_run = whole - kWideCols;
+            const uint16_t* spare = args.operands;
+            auto load_base_run = [&](u32x4 (&r)[4], int64_t n0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    r[j] = __builtin_nontemporal_load(
+                        (const u32x4_any*)(n0 < whole ? base[j] + n0 + col * 8 : spare));
+            };
+            u32x4 w[kWideRing][kLoads], y[kWideRing][4];
 #pragma unroll
             for (int j = 0; j < kWideRing; ++j) {
-                uint8_t* my_ranks = ranks[j & 1];
+                load_adapter(w[j], min(first + j * kWideCols, last_run), pieces - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                load_base_run(y[j], first + j * kWideCols);
+                __builtin_amdgcn_sched_barrier(0);   // in the order of the loop
+            }
+            for (int64_t n0 = first; n0 < whole;) {
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    if ((int)threadIdx.x + i * 256 < pieces) *(u32x4*)(my_ranks + place[i]) = w[i];
-                if (n0 + kWideCols < end) load_adapter(n0 + kWideCols);
-                __syncthreads();
-                if (wanted) {
+                for (int j = 0; j < kWideRing; ++j) {
+                    keep_adapter(ranks[j & 1], w[j]);
+                    load_adapter(w[j], min(n0 + kWideRing * kWideCols, last_run), pieces - 1);
+                    __syncthreads();
                     f32x4 d[8] = {};
+                    multiply(d, ranks[j & 1]);
 #pragma unroll
-                    for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            const u32x4 q = *(const u32x4*)(my_ranks + (t * 16 + col) * kRowPitch +
-                                                            (kh * 4 + g) * 16);
-                            d[t] = mfma(high[kh], q, d[t]);
-                            d[t] = mfma(low[kh], q, d[t]);
-                        }
-                    if (n0 < whole) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const f32x4 p = {d[0][r], d[1][r], d[2][r], d[3][r]};
-                            const f32x4 q = {d[4][r], d[5][r], d[6][r], d[7][r]};
-                            const u32x4 v = add8(y[j][r], p, q, back[r]);
-                            if (mine[r]) *(u32x4_any*)(out[r] + (n0 - first)) = v;
-                        }
-                        if (n0 + kWideRing * kWideCols < whole)
-                            load_base_run(y[j], n0 + kWideRing * kWideCols);
-                    } else {   // N ends inside this run
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const f32x4 p = {d[0][r], d[1][r], d[2][r], d[3][r]};
-                            const f32x4 q = {d[4][r], d[5][r], d[6][r], d[7][r]};
-                            const int64_t n = n0 + col * 8;
-                            if (mine[r])
-                                store_end(out[r] - mine0, n, args.N,
-                                          add8(load_end(base[r] - mine0, n, args.N), p, q, back[r]));
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        const u32x4 v = added(y[j][r], d, r);
+                        if (mine[r]) *(u32x4_any*)(out[r] + n0 + col * 8) = v;
                     }
+                    load_base_run(y[j], n0 + kWideRing * kWideCols);
+                    n0 += kWideCols;
+                    if (n0 >= whole) break;   // the same for the workgroup
                 }
-                n0 += kWideCols;
-                if (n0 >= end) break;   // the same for the workgroup
+            }
+        }
+        if (whole < end) {   // N ends inside this run
+            const int64_t from = max(first, whole);
+            u32x4 w[kLoads];
+            load_adapter(w, from, (int)min((int64_t)pieces, (args.N - from) * per_col) - 1);
+            __syncthreads();
+            keep_adapter(ranks[0], w);
+            __syncthreads();
+            f32x4 d[8] = {};
+            multiply(d, ranks[0]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t n = from + col * 8;
+                if (mine[r])
+                    store_end(out[r], n, args.N, added(load_end(base[r], n, args.N), d, r));
             }
         }
         __syncthreads();   // the next turn writes the first buffer again
