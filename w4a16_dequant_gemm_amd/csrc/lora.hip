@@ -939,22 +939,25 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
                 load_base_run(y[j], first + j * kWideCols);
                 __builtin_amdgcn_sched_barrier(0);   // in the order of the loop
             }
+            // whole rounds of the ring (a way from its first stage to itself would make that
+            // wait for the others' loads)
             for (int64_t n0 = first; n0 < whole;) {
 #pragma unroll
                 for (int j = 0; j < kWideRing; ++j) {
                     keep_adapter(ranks[j & 1], w[j]);
                     load_adapter(w[j], min(n0 + kWideRing * kWideCols, last_run), pieces - 1);
                     __syncthreads();
-                    f32x4 d[8] = {};
-                    multiply(d, ranks[j & 1]);
+                    if (n0 < whole) {
+                        f32x4 d[8] = {};
+                        multiply(d, ranks[j & 1]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const u32x4 v = added(y[j][r], d, r);
-                        if (mine[r]) *(u32x4_any*)(out[r] + n0 + col * 8) = v;
+                        for (int r = 0; r < 4; ++r) {
+                            const u32x4 v = added(y[j][r], d, r);
+                            if (mine[r]) *(u32x4_any*)(out[r] + n0 + col * 8) = v;
+                        }
                     }
                     load_base_run(y[j], n0 + kWideRing * kWideCols);
                     n0 += kWideCols;
-                    if (n0 >= whole) break;   // the same for the workgroup
                 }
             }
         }
