@@ -94,8 +94,8 @@ w4a16_status_t route_tokens_backward(const void *logits, int64_t ld, const uint8
 
 /*
  * out[t] = residual[t] + sum over j of weights[t][j] * y[places[t][j]], summed in fp32 in
- * the order of j and rounded once.  A place outside [0, R) adds nothing, and its weight
- * is not read.
+ * the order of j and rounded once.  A place outside [0, R) adds nothing, whatever its
+ * weight.
  *   y        dev, fp16 or bf16 [R] rows of N elements, ldy apart;
  *   weights  dev, float [T][top];  places  dev, int32 [T][top];
  *   residual dev, [T] rows of N, ldr apart, or NULL;  out  dev, [T][N] contiguous (it may

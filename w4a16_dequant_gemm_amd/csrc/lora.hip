@@ -1,9 +1,9 @@
 // lora.hip -- low-rank adapters of many requests beside a shared projection
 // (include/lora.h): two products, h = x A^T (K is long, R is short) and out = base +
 // h B^T (R is short, N is long), each bound by what it reads and writes: 4096 bf16 rows of 4
-// requests, K = 8192, N = 28672, R = 64: 24 us for 67 MB of x and 115-123 us for 470 MB of
-// base and out (3.8-4.1 TB/s; a copy of as much takes 88), 150 us with the order of the
-// rows (5.5) and the join of the first product's parts (5).
+// requests, K = 8192, N = 28672, R = 64: 22 us for 67 MB of x and 90 us for 470 MB of
+// base and out (5.2 TB/s, what a copy reaches), 126-136 us with the order of the rows
+// (6) and the join of the first product's parts (5).
 //
 // Rows are taken 16 at a time as columns of the matrix instruction (v_mfma_f32_16x16x32,
 // the adapter is its first operand; where there are many rows they are the first operand
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
 // at a quarter of the rate of one whose neighbouring lanes read neighbouring bytes, and
 // with many rows that rate is what counts: here x and the adapter are read in whole pieces
 // of rows and reach the matrix instruction through LDS, the adapter once for 64 rows (4096
-// rows, K = 8192, N = 28672, R = 64: 52 + 190 -> 24 + 115 us).
+// rows, K = 8192, N = 28672, R = 64: 52 + 190 -> 22 + 90 us).
 // ---------------------------------------------------------------------------
 
 constexpr int kPitch = kStep * 2 + 16;   // bytes of a row in LDS: 16 lanes touch 64 banks
@@ -800,7 +800,7 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
 }
 
 constexpr int kWideCols = 128;   // columns of a run
-constexpr int kWideRing = 2;     // runs of base in flight
+constexpr int kWideRing = 2;     // runs of base and of the adapter in flight
 
 // Second product: waves are 4 tiles of 16 rows; a run of columns of the adapter goes
 // through LDS.  h is the first operand, so a lane ends with rows g * 4 + j; the columns are
