@@ -43,7 +43,9 @@ extern "C" {
 
 /* Workspace bytes lora_add needs (0 if the arguments are bad or M is 0).  It is laid out
  * like the workspaces of w4a16_gemm, whose counters it leaves as they are, and needs no
- * fill of its own. */
+ * fill of its own.  The call is several launches that hand on through it what they found:
+ * until the last of them has run, no other call may use it, also not one that another host
+ * thread launches on the same stream (it could come between them). */
 size_t lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
                             uint32_t flags);
 

@@ -53,7 +53,9 @@ extern "C" {
 
 /* Workspace bytes route_tokens needs (0 = none, also if the arguments are bad).  It is
  * laid out like the workspaces of w4a16_gemm, whose counters it leaves as they are, and
- * needs no fill of its own. */
+ * needs no fill of its own.  The call is several launches that hand on through it what
+ * they found: until the last of them has run, no other call may use it, also not one that
+ * another host thread launches on the same stream (it could come between them). */
 size_t route_workspace_bytes(int64_t T, int64_t E, int64_t top);
 
 /*

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -349,9 +350,12 @@ def _require_workspace(workspace: torch.Tensor, where: str, device_index: int):
         _bad(f"{where}: the workspace must be a contiguous tensor on device {device_index}")
 
 
-def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.Tensor:
+def _workspace_at(nbytes: int, device_index: int, stream_handle: int,
+                  own: Optional[dict] = None) -> torch.Tensor:
+    """own: the calling thread's workspaces, in the place of those of all threads."""
     key = (device_index, stream_handle)
-    ws = _workspaces.get(key)
+    kept = _workspaces if own is None else own
+    ws = kept.get(key)
     if ws is not None and ws.numel() >= nbytes:
         return ws
     capture = _capture_number(stream_handle)
@@ -359,7 +363,7 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
         number, captured = _captured_workspaces.get(key, (None, None))
         if number == capture and captured.numel() >= nbytes:
             return captured
-    elif ws is not None:
+    elif ws is not None and own is None:
         _retired_workspaces.append(ws)
     size = 1 << 20
     while size < nbytes:
@@ -370,18 +374,32 @@ def _workspace_at(nbytes: int, device_index: int, stream_handle: int) -> torch.T
     if capture is not None:
         _captured_workspaces[key] = (capture, ws)
     else:
-        _workspaces[key] = ws
+        kept[key] = ws
     return ws
 
 
+class _Own(threading.local):
+    """A host thread's scratch memory, by (device, stream).  It goes with the thread, and a
+    smaller one with its successor: it was made on the stream of the calls that used it, so
+    what takes its place there runs after them, and no graph holds its address."""
+
+    def __init__(self):
+        self.scratch = {}
+
+
+_own = _Own()
+
+
 def _scratch(nbytes: int, device: torch.device, stream, handle: int) -> torch.Tensor:
-    """Memory for one call that needs no fill.  Calls on one stream follow one another and
-    share its workspace; a captured call gets memory of its own, since its graph may be
-    replayed beside another one, or beside calls on the stream it was captured from."""
+    """Memory for one call of several launches that needs no fill.  A thread's calls on one
+    stream follow one another and share it.  Other threads' calls, of products too, may be
+    launched between a call's kernels, so each thread has its own.  A captured call gets
+    memory of its own, since its graph may be replayed beside another one, or beside calls
+    on the stream it was captured from."""
     if (torch._C._cuda_isCurrentStreamCapturing() if stream is None
             else _capture_number(handle) is not None):
         return _empty_on(stream, nbytes, torch.uint8, device)
-    return _workspace_at(nbytes, device.index, handle)
+    return _workspace_at(nbytes, device.index, handle, _own.scratch)
 
 
 _TORCH_DT = {0: torch.float16, W4A16_BF16: torch.bfloat16}
