@@ -53,3 +53,29 @@ def test_sum_of_rows_with_all_some_and_no_slots(top, dtype):
     none = lost.all(1)
     assert int(none.sum()) >= 4
     assert torch.equal(got[none].view(torch.int16), res[none].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("E,top", [(256, 8), (100, 6), (60, 3), (16, 8), (300, 8), (100, 11)])
+@pytest.mark.parametrize("T", [64, 300])
+def test_weights_do_not_depend_on_the_tokens_beside(T, E, top, dtype):
+    """Tokens share a wave by fours; one with few logits that can be chosen, or with equal ones,
+    sends all of them another way.  The others' outputs keep their bits."""
+    say(f"weights beside other tokens T={T} E={E} top={top} {dtype}")
+    g = torch.Generator().manual_seed(E + top)
+    logits = (torch.randn(T, E, generator=g) * 2).to(DT[dtype])
+    want = rt().route_tokens(logits.cuda(), top)
+    at = torch.arange(T)
+    for what in ("few", "nan", "equal"):
+        bad = logits.clone()
+        if what == "few":
+            bad[3::4, 2:] = float("-inf")
+        elif what == "nan":
+            bad[3::4, 1:] = float("nan")
+        else:
+            bad[3::4] = 0.5
+        got = rt().route_tokens(bad.cuda(), top)
+        keep = at % 4 != 3
+        assert torch.equal(got.experts.cpu()[keep], want.experts.cpu()[keep]), what
+        assert torch.equal(got.weights.cpu()[keep].view(torch.int32),
+                           want.weights.cpu()[keep].view(torch.int32)), what

@@ -92,6 +92,19 @@ __device__ __forceinline__ uint32_t group_max_bits(uint32_t x) {
 }
 
 template <int G>
+__device__ __forceinline__ uint32_t group_sum_bits(uint32_t x) {
+    x += dpp_bits<kXor1>(x);
+    x += dpp_bits<kXor2>(x);
+    x += dpp_bits<kHalfMirror>(x);
+    x += dpp_bits<kMirror>(x);
+    if constexpr (G == 64) {
+        x += (uint32_t)__shfl_xor((int)x, 16, 64);
+        x += (uint32_t)__shfl_xor((int)x, 32, 64);
+    }
+    return x;
+}
+
+template <int G>
 __device__ __forceinline__ float group_sum(float x) {
     x += dpp<kXor1>(x);
     x += dpp<kXor2>(x);
@@ -400,6 +413,8 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_ke
 #pragma unroll
         for (int i = 0; i < PER; ++i) sums[i] = 0.0f;
     }
+    const float step = top <= 8 ? 0x1p28f : 0x1p26f;
+    auto steps_of = [&](float x) { return (uint32_t)fmaxf(x * step, 0.0f); };   // NaN: 0
     for (int round = 0; round < here; round += threads / G) {
         const int t = round + group;
         const bool live = t < here && (!a.valid || a.valid[first + t]);
@@ -416,10 +431,14 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_ke
 #pragma unroll
             for (int i = 0; i < PER; ++i) sums[i] = __builtin_fmaf(p[i], inv, sums[i]);
         }
-        float taken = 0.0f;
+        // The chosen exponentials' sum, between 1 and top, in steps of 2^-28 (more than 8: 2^-26): a
+        // whole number, so that the order in which they are found, which the wave's other
+        // tokens have a part in, does not count.  Each loses less than a step; adding it in
+        // fp32 would lose up to 2^-24 and more of them the larger the sum.
+        uint32_t taken = 0;
         auto choose = [&](int j, bool win, int e, float l) {   // l: the chosen logit, the group's
             const float x = l > -kInf ? exp_down(l - base) : 0.0f;
-            taken += x;
+            taken += steps_of(x);
             if (t >= here) return;
             if (win) {
                 chosen[t * top + j] = (uint16_t)e;
@@ -471,7 +490,7 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_ke
                     for_others(key, [&](Key other) { place += other > key; });
                     const bool win = any && place < top;
                     const float x = win ? exp_down(l - base) : 0.0f;
-                    taken = group_sum<G>(x);
+                    taken = group_sum_bits<G>(steps_of(x));
                     if (win) {
                         chosen[t * top + place] = (uint16_t)e;
                         weight[t * top + place] = x;
@@ -534,7 +553,7 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kTileThreads, 4) void choose_ke
         }
         if (g == 0 && t < here) {
             // a NaN of the row is in sum
-            factor[t] = !a.renormalize ? inv : sum == sum ? inverse(taken) : sum;
+            factor[t] = !a.renormalize ? inv : sum == sum ? inverse((float)taken) * step : sum;
             if (live) atomicAdd(&part[16], 1);
         }
     }
