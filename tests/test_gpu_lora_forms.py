@@ -1,0 +1,44 @@
+"""GPU tests of the low-rank adapters (include/lora.h): numbers at the ends of the types, and the
+forms that their plans take for certain sizes, against the definition in 64 bits."""
+import pytest
+
+from gpu_helpers import lib, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    lib()
+
+
+def lr():
+    from w4a16_dequant_gemm_amd import lora
+    return lora
+
+
+# few rows, ordered rows, and both forms for many rows; ranks that fill an operand and not
+FORMS = [(3, 16), (3, 40), (200, 40), (600, 64), (600, 40), (1100, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,R", FORMS)
+def test_infinite_scale(M, R, dtype):
+    """All numbers of h and b are positive: infinite is what comes out, whatever lies behind the
+    last rank; other adapters' rows are not touched by it."""
+    say(f"infinite scale M={M} R={R} {dtype}")
+    N, K = 200, 64
+    x = torch.full((M, K), 0.5, dtype=DT[dtype]).cuda()
+    a = torch.full((2, R, K), 0.25, dtype=DT[dtype]).cuda()
+    b = torch.full((2, N, R), 0.125, dtype=DT[dtype]).cuda()
+    base = torch.ones(M, N, dtype=DT[dtype]).cuda()
+    ids = (torch.arange(M) % 2).to(torch.int32).cuda()
+    out = lr().lora_add(base, x, a, b, ids, scale=torch.tensor([INF, 1.0]).cuda())
+    assert bool((out[ids == 0] == INF).all())
+    assert bool((out[ids == 1] == 1.0 + R).all())      # 64 / 8 / 8 ranks of one each

@@ -382,10 +382,11 @@ __device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[K
                 p += *(const f32x4*)(h + s * next);
                 q += *(const f32x4*)(h + s * next + 4);
             }
+            p *= scale, q *= scale;   // not the zeros behind R: scale may be infinite
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[kh][i] = (i < 4 ? p[i] : q[i - 4]) * scale;
+            v[kh][i] = i < 4 ? p[i] : q[i - 4];
             most = fmaxf(most, fabsf(v[kh][i]));
         }
     }
@@ -771,12 +772,10 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
                 for (int k = 0; k < 4; ++k) sum[i] += p[k];
             }
             for (; s < args.splits; ++s) sum[i] += *(const f32x4*)(h + s * args.P * args.R);
+            sum[i] *= scale;   // not the zeros behind R: scale may be infinite
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            sum[i][k] *= scale;
-            most = fmaxf(most, fabsf(sum[i][k]));
-        }
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, fabsf(sum[i][k]));
     }
     float by = 1.0f;
     if constexpr (!BF16) {
