@@ -42,3 +42,21 @@ def test_infinite_scale(M, R, dtype):
     out = lr().lora_add(base, x, a, b, ids, scale=torch.tensor([INF, 1.0]).cuda())
     assert bool((out[ids == 0] == INF).all())
     assert bool((out[ids == 1] == 1.0 + R).all())      # 64 / 8 / 8 ranks of one each
+
+
+@pytest.mark.parametrize("M,R", FORMS)
+def test_infinite_rank_beside_large_ones_fp16(M, R):
+    """One inner product is infinite, the others lie beyond fp16: an infinity comes out, since
+    all of b is positive; where b's number for that rank is zero, NaN, as by the definition."""
+    say(f"infinite rank M={M} R={R}")
+    N, K = 200, 64
+    x = torch.full((M, K), 256.0, dtype=torch.float16).cuda()
+    a = torch.full((1, R, K), 128.0, dtype=torch.float16)
+    a[0, R // 2, 5] = INF
+    b = torch.full((1, N, R), 0.5, dtype=torch.float16)
+    b[0, 77, R // 2] = 0.0
+    out = lr().lora_add(torch.ones(M, N, dtype=torch.float16).cuda(), x, a.cuda(), b.cuda(),
+                        torch.zeros(M, dtype=torch.int32).cuda())
+    rest = torch.arange(N) != 77
+    assert bool((out[:, rest.cuda()] == INF).all())
+    assert bool(torch.isnan(out[:, 77]).all())

@@ -343,11 +343,17 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4& high, u32x4& 
     }
 }
 
-// The power of two that brings fp16's rows, whose largest number is `most`, to below 2^14,
-// where neither part leaves the type's range; back: its reciprocal.
+// The larger of the two magnitudes, v's if it is finite: infinities stay what they are under
+// any power of two, and beside them the other numbers must not become infinite too.
+__device__ __forceinline__ float larger(float most, float v) {
+    return finite(v) ? fmaxf(most, fabsf(v)) : most;
+}
+
+// The power of two that brings fp16's rows, whose largest finite number is `most`, to below
+// 2^14, where neither part leaves the type's range; back: its reciprocal.
 [[maybe_unused]] __device__ __forceinline__ float power_for(float most, float& back) {
-    const int e = (int)(__float_as_uint(most) >> 23) - 127;   // 128: not finite
-    const int shift = e == 128 ? 0 : min(13 - e, 120);
+    const int e = (int)(__float_as_uint(most) >> 23) - 127;
+    const int shift = min(13 - e, 120);
     back = __uint_as_float((uint32_t)(127 - shift) << 23);
     return __uint_as_float((uint32_t)(127 + shift) << 23);
 }
@@ -387,7 +393,7 @@ __device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[K
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[kh][i] = i < 4 ? p[i] : q[i - 4];
-            most = fmaxf(most, fabsf(v[kh][i]));
+            most = larger(most, v[kh][i]);
         }
     }
     float back = 1.0f;
@@ -775,7 +781,7 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
             sum[i] *= scale;   // not the zeros behind R: scale may be infinite
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) most = fmaxf(most, fabsf(sum[i][k]));
+        for (int k = 0; k < 4; ++k) most = larger(most, sum[i][k]);
     }
     float by = 1.0f;
     if constexpr (!BF16) {
