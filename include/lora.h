@@ -9,10 +9,10 @@
  * id is outside [0, L) has no adapter: out[m] = base[m], bit for bit.  The rows of an
  * adapter may lie anywhere; what an adapter or a row holds (NaN and infinities too) is
  * seen in that adapter's or row's outputs only.  The R inner products with A are kept in
- * fp32; as operand of the second product each is split into two numbers of the
- * activations' type (fp16: after a row's were brought near 2^14 by a power of two), which
- * keeps 17 (bf16) or 22 (fp16) of its bits.  Sums have a fixed order: equal calls
- * give equal bits, and a row's result does not depend on the other rows' ids.
+ * fp32; as operand of the second product each is the sum of numbers of the activations'
+ * type: bf16 of three, which hold all its 24 bits, fp16 of two, which hold 22 (after a row's
+ * finite ones were brought near 2^14 by a power of two).  Sums have a fixed order: equal
+ * calls give equal bits, and a row's result does not depend on the other rows' ids.
  *
  * Conventions are those of w4a16.h (plain C types, caller-owned device pointers, stream
  * as void*, asynchronous, nothing allocated, every argument validated on the host before

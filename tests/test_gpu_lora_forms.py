@@ -60,3 +60,49 @@ def test_infinite_rank_beside_large_ones_fp16(M, R):
     rest = torch.arange(N) != 77
     assert bool((out[:, rest.cuda()] == INF).all())
     assert bool(torch.isnan(out[:, 77]).all())
+
+
+@pytest.mark.parametrize("M,R", FORMS)
+def test_inner_products_of_24_bits_bf16(M, R):
+    """Pairs of ranks whose inner products are whole numbers below 2^24 that share their upper 16
+    bits, added and taken away by b: every step is exact in fp32, and what is left are the
+    lower 8 bits."""
+    say(f"inner products of 24 bits M={M} R={R}")
+    N, K = 200, 64
+    g = torch.Generator().manual_seed(M + R)
+    x = torch.zeros(M, K)
+    x[:, 3], x[:, 9], x[:, 40] = 2.0 ** 16, 2.0 ** 8, 1.0
+    parts = torch.randint(1, 256, (2, R // 2, 3), generator=g)
+    a = torch.zeros(2, R, K)
+    a[:, 0::2, 3] = a[:, 1::2, 3] = parts[..., 0].float()
+    a[:, 0::2, 9] = a[:, 1::2, 9] = parts[..., 1].float()
+    a[:, 0::2, 40] = parts[..., 2].float()
+    pair = torch.arange(N) % (R // 2)
+    b = torch.zeros(2, N, R)
+    b[:, torch.arange(N), 2 * pair] = 1.0
+    b[:, torch.arange(N), 2 * pair + 1] = -1.0
+    ids = torch.arange(M) % 3 % 2
+    out = lr().lora_add(*(t.to(torch.bfloat16).cuda() for t in (torch.zeros(M, N), x, a, b)),
+                        ids.to(torch.int32).cuda()).cpu()
+    assert torch.equal(out.float(), parts[ids][:, pair, 2].float())
+
+
+@pytest.mark.parametrize("M,R", FORMS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_inner_products_beyond_bf16(M, R, sign):
+    """Inner products between bf16's largest number and fp32's, brought back by b: the definition's
+    outputs are ordinary numbers."""
+    say(f"inner products beyond bf16 M={M} R={R} sign={sign}")
+    N, K = 200, 64
+    x, a = torch.zeros(M, K), torch.zeros(1, R, K)
+    x[:, 1], a[:, :, 1] = sign * 1.9921875 * 2.0 ** 63, 1.9921875 * 2.0 ** 63
+    x[:, 5], a[:, :, 5] = sign * 2.0 ** 63, 1.5 * 2.0 ** 57
+    b = torch.zeros(1, N, R)
+    b[0, torch.arange(N), torch.arange(N) % R] = 2.0 ** -100
+    x, a, b = (t.to(torch.bfloat16) for t in (x, a, b))
+    h = x.double() @ a[0].double().t()
+    assert 3.3961e38 < float(h.abs().max()) < 3.4028e38
+    out = lr().lora_add(torch.zeros(M, N, dtype=torch.bfloat16).cuda(), x.cuda(), a.cuda(),
+                        b.cuda(), torch.zeros(M, dtype=torch.int32).cuda()).cpu()
+    want = h @ b[0].double().t()
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -20) * want.abs()).all())

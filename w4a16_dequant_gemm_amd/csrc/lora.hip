@@ -317,29 +317,44 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_kernel(LoraArgs args) {
 // ---------------------------------------------------------------------------
 // Second product.  Wave: 16 rows and runs of 64 columns, in order; the waves of a workgroup
 // lie side by side in rows where there are many, so that they find the adapter's numbers
-// in the L1.  h is split into a high and a low part of 16 bits each, so that the matrix
-// instruction loses nothing that the output could hold.  One row of N = 4096 takes 4.1 us; 64
-// rows over 32 adapters, N = 28672, R = 16 (30 MB of b) 14-16 us: a load of b stands in 16
-// rows, and an adapter's numbers are read again for each tile that has a row of it.
+// in the L1.  h is the sum of numbers of 16 bits each, as the matrix instruction takes them:
+// of three in bf16, which hold all of it (two hold 17 of its 24 bits: 12 times the error of a
+// product in fp32 where base takes most of h B^T away), of two in fp16.  One row of
+// N = 4096 takes 4.1 us; 64 rows over 32 adapters, N = 28672, R = 16 (30 MB of b) 14-16 us: a
+// load of b stands in 16 rows, and an adapter's numbers are read again for each tile that
+// has a row of it.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
-// A number as two 16-bit ones whose sum it is (to 17 bits bf16, 22 bits fp16); what is not
-// finite stands in the high one alone.
-__device__ __forceinline__ void split(float v, uint32_t& high, uint32_t& low) {
-    high = to_half(v);
-    low = finite(v) ? to_half(v - to_float(high)) : 0u;
+constexpr int kParts = BF16 ? 3 : 2;
+
+// A number as kParts 16-bit ones whose sum it is: bf16 exactly (8 of its 24 bits in each; cut
+// off, not rounded, so that none leaves the type's range), fp16 to 22 bits.  What is not
+// finite stands in the first alone.
+__device__ __forceinline__ void split(float v, uint32_t (&part)[kParts]) {
+    if constexpr (BF16) {
+        constexpr uint32_t kHigh = 0xFFFF0000u;
+        const uint32_t bits = __float_as_uint(v);
+        const float rest = finite(v) ? v - __uint_as_float(bits & kHigh) : 0.0f;
+        const uint32_t next = __float_as_uint(rest);
+        part[0] = bits >> 16;
+        part[1] = next >> 16;
+        part[2] = __float_as_uint(rest - __uint_as_float(next & kHigh)) >> 16;
+    } else {
+        part[0] = to_half(v);
+        part[1] = finite(v) ? to_half(v - to_float(part[0])) : 0u;
+    }
 }
 
-__device__ __forceinline__ void split8(const float (&v)[8], u32x4& high, u32x4& low) {
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4 (&part)[kParts]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t h0, l0, h1, l1;
-        split(v[2 * i], h0, l0);
-        split(v[2 * i + 1], h1, l1);
-        high[i] = h0 | h1 << 16;
-        low[i] = l0 | l1 << 16;
+        uint32_t even[kParts], odd[kParts];
+        split(v[2 * i], even);
+        split(v[2 * i + 1], odd);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) part[p][i] = even[p] | odd[p] << 16;
     }
 }
 
@@ -358,12 +373,11 @@ __device__ __forceinline__ float larger(float most, float v) {
     return __uint_as_float((uint32_t)(127 + shift) << 23);
 }
 
-// A row's h (lane group g: every fourth run of 8 ranks) into operands, splits of a number
+// A row's h (lane group g: every fourth run of 8 ranks) into operands, parts of K
 // four at a time; returns what the product has to be multiplied by.
 template <int KH>
-__device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[KH],
-                                               const LoraArgs& args, int64_t row, int adapter,
-                                               int g) {
+__device__ __forceinline__ float make_operands(u32x4 (&part)[KH][kParts], const LoraArgs& args,
+                                               int64_t row, int adapter, int g) {
     const float scale = args.scale ? args.scale[adapter] : 1.0f;
     float v[KH][8], most = 0.0f;
 #pragma unroll
@@ -407,7 +421,7 @@ __device__ __forceinline__ float make_operands(u32x4 (&high)[KH], u32x4 (&low)[K
             for (int i = 0; i < 8; ++i) v[kh][i] *= by;
     }
 #pragma unroll
-    for (int kh = 0; kh < KH; ++kh) split8(v[kh], high[kh], low[kh]);
+    for (int kh = 0; kh < KH; ++kh) split8(v[kh], part[kh]);
     return back;
 }
 
@@ -470,8 +484,8 @@ __device__ __forceinline__ void load_base(u32x4 (&y)[2], const uint16_t* base, i
 }
 
 template <int KH>
-__device__ __forceinline__ void multiply(f32x4 (&d)[4], u32x4 (&w)[4][KH], const u32x4 (&high)[KH],
-                                         const u32x4 (&low)[KH], int R, int g) {
+__device__ __forceinline__ void multiply(f32x4 (&d)[4], u32x4 (&w)[4][KH],
+                                         const u32x4 (&part)[KH][kParts], int R, int g) {
     const uint32_t keep = ((KH - 1) * 4 + g) * 8 < R ? ~0u : 0u;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -479,13 +493,11 @@ __device__ __forceinline__ void multiply(f32x4 (&d)[4], u32x4 (&w)[4][KH], const
         d[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int kh = 0; kh < KH; ++kh)
+    for (int p = 0; p < kParts; ++p)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) d[t] = mfma(w[t][kh], high[kh], d[t]);
+        for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-    for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) d[t] = mfma(w[t][kh], low[kh], d[t]);
+            for (int t = 0; t < 4; ++t) d[t] = mfma(w[t][kh], part[kh][p], d[t]);
 }
 
 template <bool WHOLE>
@@ -555,15 +567,15 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
             if (first + j * kUpCols < whole)
                 load_base<true>(y[j], base, first + j * kUpCols, args.N, g);
 
-        u32x4 high[KH], low[KH];
-        const float back = make_operands<KH>(high, low, args, row, adapter, g);
+        u32x4 parts[KH][kParts];
+        const float back = make_operands<KH>(parts, args, row, adapter, g);
 
         f32x4 d[4];
         int64_t n0 = first;
         while (n0 < whole) {
 #pragma unroll
             for (int j = 0; j < kRing; ++j) {
-                multiply<KH>(d, w, high, low, args.R, g);
+                multiply<KH>(d, w, parts, args.R, g);
                 if (n0 + kUpCols < whole)
                     load_adapter<KH, true>(w, b, n0 + kUpCols, args.N, args.R, col, g);
                 add_run<true>(d, y[j], back, out, mine, n0, args.N, g);
@@ -576,7 +588,7 @@ __global__ __launch_bounds__(kUpWaves* 64, KH <= 2 ? 3 : 1) void up_kernel(LoraA
         if (n0 < end) {   // N ends inside this run
             load_adapter<KH, false>(w, b, n0, args.N, args.R, col, g);
             load_base<false>(y[0], base, n0, args.N, g);
-            multiply<KH>(d, w, high, low, args.R, g);
+            multiply<KH>(d, w, parts, args.R, g);
             add_run<false>(d, y[0], back, out, mine, n0, args.N, g);
         }
     }
@@ -747,8 +759,8 @@ __global__ __launch_bounds__(512, 2) void down_wide_kernel(LoraArgs args) {
     }
 }
 
-// The parts of h into the second product's operands: sums over the splits times the
-// adapter's scale, as high and low parts, ranks filled up to whole operands with zeros.
+// The parts of h joined for the second product: sums over the splits times the adapter's scale
+// (fp16: and the row's power of two), ranks filled up to whole operands with zeros.
 // 16 lanes per row.  (Up to 500 rows every wave of the second product does this for itself:
 // there it costs less than a launch.)
 template <int KH>
@@ -791,16 +803,11 @@ __global__ __launch_bounds__(256) void join_kernel(LoraArgs args) {
         by = power_for(most, back);
         if (lane == 0) args.back[row] = back;
     }
-    uint16_t* out = args.operands + row * (KH * 64);
+    float* out = args.operands + row * (KH * 32);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int rank = i * 64 + lane * 4;
-        if (rank >= KH * 32) continue;
-        uint32_t high[4], low[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split(sum[i][k] * by, high[k], low[k]);
-        *(u32x2*)(out + rank) = u32x2{high[0] | high[1] << 16, high[2] | high[3] << 16};
-        *(u32x2*)(out + KH * 32 + rank) = u32x2{low[0] | low[1] << 16, low[2] | low[3] << 16};
+        if (rank < KH * 32) *(f32x4*)(out + rank) = sum[i] * by;
     }
 }
 
@@ -895,30 +902,42 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
             base[j] = (const uint16_t*)args.base + row * args.ldb;
             out[j] = (uint16_t*)args.out + row * args.ldo;
         }
-        u32x4 high[KH], low[KH];
+        u32x4 part[KH][kParts];
         float back[4] = {1.0f, 1.0f, 1.0f, 1.0f};
         {
             const int64_t row = min(tile0 + (tile_rows >> col & 1 ? col : one_row), args.P - 1);
-            const uint16_t* h = args.operands + row * (KH * 64) + g * 8;
+            const float* h = args.operands + row * (KH * 32) + g * 8;
 #pragma unroll
             for (int kh = 0; kh < KH; ++kh) {
-                high[kh] = *(const u32x4*)(h + kh * 32);
-                low[kh] = *(const u32x4*)(h + (KH + kh) * 32);
+                const f32x4 p = *(const f32x4*)(h + kh * 32), q = *(const f32x4*)(h + kh * 32 + 4);
+                const float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+                split8(v, part[kh]);
             }
             if constexpr (!BF16)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     back[j] = args.back[min(tile0 + (mine[j] ? g * 4 + j : one_row), args.P - 1)];
         }
+        // operands of the adapter a few at a time, each part of h with all of them: products that
+        // follow one another do not wait for each other's sums (bf16's third part costs 4096
+        // rows R = 128 nothing, 222 -> 218 us; one after the other 239).  Up to 3 operands
+        // 4 at a time would cost waves.
         auto multiply = [&](f32x4 (&d)[8], const uint8_t* my_ranks) {
+            constexpr int kAtOnce = KH <= 3 ? 2 : 4;
 #pragma unroll
             for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const u32x4 q = *(const u32x4*)(my_ranks + (t * 16 + col) * kRowPitch +
-                                                    (kh * 4 + g) * 16);
-                    d[t] = mfma(high[kh], q, d[t]);
-                    d[t] = mfma(low[kh], q, d[t]);
+                for (int t0 = 0; t0 < 8; t0 += kAtOnce) {
+                    u32x4 q[kAtOnce];
+#pragma unroll
+                    for (int t = 0; t < kAtOnce; ++t)
+                        q[t] = *(const u32x4*)(my_ranks + ((t0 + t) * 16 + col) * kRowPitch +
+                                               (kh * 4 + g) * 16);
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int t = 0; t < kAtOnce; ++t)
+                            d[t0 + t] = mfma(part[kh][p], q[t], d[t0 + t]);
                 }
         };
         auto added = [&](u32x4 q, const f32x4 (&d)[8], int r) {
@@ -929,7 +948,7 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
             // runs behind the last one's are read too (the adapter's last, a piece of h for
             // base), so that every load and its place in the order are known
             const int64_t last_run = whole - kWideCols;
-            const uint16_t* spare = args.operands;
+            const uint16_t* spare = (const uint16_t*)args.operands;
             auto load_base_run = [&](u32x4 (&r)[4], int64_t n0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

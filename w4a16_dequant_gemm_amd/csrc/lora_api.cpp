@@ -150,7 +150,7 @@ w4a16_status_t lora_add(const void* base, int64_t ldb, const void* x, int64_t ld
     if (!aligned(workspace, 16)) return W4A16_ERR_INVALID_ARG;
     uint8_t* scratch = (uint8_t*)workspace + kSkip;
     a.h = (float*)scratch;
-    a.operands = (uint16_t*)(scratch + need.operands);
+    a.operands = (float*)(scratch + need.operands);
     a.back = (float*)(scratch + need.back);
     if (a.by_adapter) {
         a.order = (int32_t*)(scratch + need.order);

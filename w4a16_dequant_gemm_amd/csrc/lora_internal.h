@@ -27,9 +27,9 @@ struct LoraArgs {
     int32_t* order;       // [P] rows by adapter (null: as they are), and their ids
     int32_t* sorted;
     float* h;             // [splits][P][R]: partial inner products with A
-    // many rows: operands of the second product, [P][2][R filled up to 32], and (fp16) what
-    // a row's products are multiplied by
-    uint16_t* operands;
+    // many rows: the sums over the parts, [P][R filled up to 32], and (fp16) what a row's
+    // products are multiplied by
+    float* operands;
     float* back;
     int64_t ldb, ldx, ldo, M, N, K;
     int64_t P;            // places of rows
