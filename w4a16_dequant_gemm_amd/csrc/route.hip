@@ -918,11 +918,10 @@ __global__ __launch_bounds__(kBackThreads) void back_kernel(BackArgs a) {
 template <int G, int PER, bool LOSS>
 hipError_t choose(const RouteArgs& a, hipStream_t stream) {
     // one tile: one pass over it if its lanes fit a workgroup; several: workgroups of 256, of
-    // which a CU holds more at once (65536 x 256 fp32: 58 -> 48 us).  The waves'
-    // sums of p stay within 32 KiB
-    int threads = (int)min((int64_t)(a.tiles == 1 ? kOneThreads : kTileThreads), ((int64_t)a.tile * G + 63) / 64 * 64);
-    if (LOSS)
-        while (threads > 64 && threads / 64 * a.E * 4 > 32768) threads = threads / 128 * 64;
+    // which a CU holds more at once (65536 x 256 fp32: 58 -> 48 us)
+    const int64_t most = a.tiles == 1 ? kOneThreads : kTileThreads;
+    const int threads = (int)min(most, ((int64_t)a.tile * G + 63) / 64 * 64);
+    static_assert(kOneThreads / 64 * ROUTE_MAX_EXPERTS * 4 <= 32768, "the waves' sums of p in LDS");
     const int bytes = shared_of(a.E, a.top, a.tile, threads, LOSS).bytes;
     if (a.tiles == 1)
         choose_kernel<G, PER, LOSS, true><<<1, threads, bytes, stream>>>(a);
