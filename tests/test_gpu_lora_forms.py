@@ -106,3 +106,123 @@ def test_inner_products_beyond_bf16(M, R, sign):
                         b.cuda(), torch.zeros(M, dtype=torch.int32).cuda()).cpu()
     want = h @ b[0].double().t()
     assert bool(((out.double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -20) * want.abs()).all())
+
+
+# ---- forms that the plans take for certain sizes
+#
+# Bar, as at the head of test_gpu_lora.py, with U = 2^-24 and S = sum over ranks of |scale| (sum
+# over k |x a|) |b|: K + 40 steps of fp32 in the first sum and its joins, 3 R (bf16: every part of
+# a number counts) or 2 R (fp16) in the second, each counted twice; fp16 also 2^-22 of S and
+# 2^-38 of the row's largest for what two parts leave out; then half a step of the output.
+
+U = 2.0 ** -24
+
+
+def check(got, p, dtype):
+    want, S, top = define(p)
+    K, R = p["x"].shape[1], p["a"].shape[1]
+    if dtype == "bf16":
+        delta = 2 * (K + 40 + 3 * R) * U * S
+    else:
+        delta = (2 * (K + 40 + 2 * R) * U + 2.0 ** -22) * S + 2.0 ** -38 * top
+    f = torch.finfo(DT[dtype])
+    bound = delta * (1 + f.eps / 2) + (f.eps / 2 + 2 * U) * want.abs() \
+        + f.smallest_normal * f.eps / 2
+    off = (got.double() - want).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
+    without = (p["ids"] < 0) | (p["ids"] >= p["a"].shape[0])
+    assert torch.equal(got[without].view(torch.int16), p["base"][without].view(torch.int16))
+
+
+def define(p):
+    """(out, S, the row's largest |h| times sum |b|) in 64 bits, over the adapters that are used."""
+    x = p["x"].double()
+    if p["xs"] is not None:
+        x = x * p["xs"].double().repeat_interleave(128, 1)[:, :x.shape[1]]
+    out = p["base"].double()
+    S, top = torch.zeros_like(out), torch.zeros_like(out)
+    for a in p["ids"].unique().tolist():
+        if not 0 <= a < p["a"].shape[0]:
+            continue
+        m = (p["ids"] == a).nonzero()[:, 0]
+        A, B, scale = p["a"][a].double(), p["b"][a].double(), p["scale"][a].double()
+        h = x[m] @ A.t() * scale
+        out[m] += h @ B.t()
+        S[m] = (x[m].abs() @ A.abs().t() * scale.abs()) @ B.abs().t()
+        top[m] = h.abs().amax(1, keepdim=True) * B.abs().sum(1)
+    return out, S, top
+
+
+def problem(M, N, K, R, L, dtype, rows, ids):
+    t, g = DT[dtype], torch.Generator(device="cuda")
+    g.manual_seed(M + N + K + R + L)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+    x, xs = randn(M, K), None
+    if rows == "fp8":
+        xs = torch.rand(M, -(-K // 128), generator=g, device="cuda") * 0.01 + 0.001
+        x = (x * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    else:
+        x = x.to(t)
+    return dict(base=randn(M, N).to(t), x=x, xs=xs, ids=ids.to(torch.int32).cuda(),
+                a=(randn(L, R, K) * K ** -0.5).to(t), b=(randn(L, N, R) * R ** -0.5).to(t),
+                scale=torch.rand(L, generator=g, device="cuda") * 2 - 0.5)
+
+
+def splits_of(M, N, K, R, L):
+    """Parts of K in the plan for many rows, from the workspace that it asks for."""
+    places = (M // 64 + L + 1) * 64 if 1 < L <= 64 else M
+    fixed = places * ((R + 31) // 32 * 128 + 4 + (8 if L > 1 else 0))
+    parts = (lr().lora_workspace_bytes(M, N, K, R, L, 0) - 65536 - fixed) / (places * R * 4)
+    assert parts == int(parts)
+    return int(parts)
+
+
+# (shape, parts of K): first products whose loads run on past the first stages, joins of four
+# parts and more, second products of 1 to 5 runs of columns a workgroup with whole and
+# ragged ends, and every number of operands of 32 ranks
+MANY = [((1030, 4200, 8208, 64, 3), 11), ((1030, 9000, 8208, 64, 3), 11),
+        ((3000, 9000, 2064, 64, 3), 5), ((3000, 5130, 1040, 64, 3), 3),
+        ((2000, 20000, 528, 64, 2), 2), ((2100, 19968, 528, 16, 1), 2),
+        ((600, 1000, 8208, 136, 3), 7), ((600, 1000, 4112, 168, 3), 6),
+        ((600, 3001, 4112, 256, 3), 5), ((600, 500, 4112, 112, 2), 9)]
+
+
+@pytest.mark.parametrize("rows", ["x16", "fp8"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape,splits", MANY)
+def test_many_rows(shape, splits, dtype, rows):
+    M, N, K, R, L = shape
+    say(f"many rows M={M} N={N} K={K} R={R} L={L} {dtype} {rows}")
+    assert splits_of(*shape) == splits
+    ids = torch.arange(M) // 37 % (L + 1) - 1 if L > 1 else torch.zeros(M)
+    p = problem(M, N, K, R, L, dtype, rows, ids)
+    check(lr().lora_add(**p), p, dtype)
+
+
+# more adapters than groups are made for: ordered rows of several adapters in a group, in both
+# forms for many rows and in the one for few; above 1023 they share bins of the order
+MIXED = [(600, 400, 1040, 64, 100), (600, 401, 1040, 64, 1500), (4000, 130, 528, 24, 100),
+         (600, 400, 1040, 16, 1500), (200, 130, 2064, 40, 66), (130, 1000, 144, 16, 100),
+         (520, 70, 48, 200, 1100)]
+
+
+@pytest.mark.parametrize("rows", ["x16", "fp8"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,N,K,R,L", MIXED)
+def test_many_adapters(M, N, K, R, L, dtype, rows):
+    g = torch.Generator().manual_seed(M + L)
+    for how in ("random", "colliding"):
+        say(f"many adapters M={M} N={N} K={K} R={R} L={L} {dtype} {rows} {how}")
+        ids = torch.randint(-1, L, (M,), generator=g)
+        if how == "colliding":     # few remainders of 1023, several adapters each
+            ids = torch.tensor([i for i in (0, 1023, 5, 1028, 64, 65, -1) if i < L])[
+                torch.randint(0, 100, (M,), generator=g) % (7 if L > 1028 else 5)]
+        ids[::17] = L + 5
+        p = problem(M, N, K, R, L, dtype, rows, ids)
+        got = lr().lora_add(**p)
+        check(got, p, dtype)
+        base = p["base"]
+        p["base"] = base.clone()
+        assert torch.equal(lr().lora_add(**p, out=p["base"]), got)
