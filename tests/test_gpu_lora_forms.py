@@ -226,3 +226,21 @@ def test_many_adapters(M, N, K, R, L, dtype, rows):
         base = p["base"]
         p["base"] = base.clone()
         assert torch.equal(lr().lora_add(**p, out=p["base"]), got)
+
+
+# more rows than the order keeps in registers; one adapter, whose rows are not ordered, with
+# groups of rows that have none
+@pytest.mark.parametrize("rows", ["x16", "fp8"])
+@pytest.mark.parametrize("M,N,K,R,L", [(9300, 70, 48, 16, 40), (9300, 70, 48, 40, 1500),
+                                       (20000, 9, 16, 8, 300), (600, 300, 272, 64, 1),
+                                       (1100, 300, 272, 16, 1), (300, 300, 272, 64, 1)])
+def test_order_of_many_rows_and_none(M, N, K, R, L, rows):
+    say(f"order M={M} N={N} K={K} R={R} L={L} {rows}")
+    g = torch.Generator().manual_seed(M)
+    ids = torch.randint(-1, L, (M,), generator=g)
+    ids[M // 3:M // 3 + 150] = -1
+    p = problem(M, N, K, R, L, "bf16", rows, ids)
+    got = lr().lora_add(**p)
+    check(got, p, "bf16")
+    base = p["base"].clone()
+    assert torch.equal(lr().lora_add(**{**p, "base": base}, out=base), got)

@@ -3,6 +3,7 @@ take for certain sizes, types and masks, and what must hold between them."""
 import pytest
 
 from gpu_helpers import lib, say
+from test_gpu_route import check_routing, define, define_backward, make_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,86 @@ def test_weights_do_not_depend_on_the_tokens_beside(T, E, top, dtype):
         assert torch.equal(got.experts.cpu()[keep], want.experts.cpu()[keep]), what
         assert torch.equal(got.weights.cpu()[keep].view(torch.int32),
                            want.weights.cpu()[keep].view(torch.int32)), what
+
+
+# ---- sizes from which the kernels go on in another way
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,E,top", [(40000, 60, 6), (20000, 256, 8), (70000, 130, 3),
+                                     (5000, 1000, 8)])
+def test_route_backward_of_several_tokens_a_group(T, E, top, dtype):
+    """More tokens than groups of lanes are there at once: each takes several in turn, with what
+    the weights pull at in the same memory and the loss's slopes kept.  Bar: as in
+    test_gpu_route.py."""
+    say(f"route backward T={T} E={E} top={top} {dtype}")
+    logits = make_logits(T, E, dtype, T)
+    g = torch.Generator().manual_seed(E)
+    valid, a = torch.rand(T, generator=g) > 0.2, torch.randn(T, top, generator=g)
+    for renormalize in (True, False):
+        want = define(logits, top, renormalize, valid)
+        r = rt().route_tokens(logits.cuda(), top, renormalize=renormalize, balance=True,
+                              valid=valid.cuda())
+        check_routing(r, want, True)
+        got = rt().route_tokens_backward(logits.cuda(), r, a.cuda(),
+                                         torch.tensor(40.0, device="cuda"))
+        d, m = define_backward(want, a.double(), 40.0, renormalize)
+        bound = (4 * min(want["D"], 104.0) + 160) * U * m + HALF[dtype] * d.abs() + TINY[dtype]
+        assert bool(((got.cpu().double() - d).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,top,N", [(2049, 2, 1031), (3000, 5, 4099), (2048, 2, 4099),
+                                     (4000, 9, 72)])
+def test_combine_backward_of_many_tokens(T, top, N, dtype):
+    """Workgroups of 256 up to 2048 tokens, of 512 above.  Bar: as in test_gpu_route.py."""
+    say(f"combine backward T={T} top={top} N={N} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N)
+    y = torch.randn(T * top, N, generator=g, device="cuda").to(DT[dtype])
+    dout = torch.randn(T, N, generator=g, device="cuda").to(DT[dtype])
+    w = torch.randn(T, top, generator=g, device="cuda")
+    slots = torch.arange(T * top, device="cuda")
+    lost = torch.rand(T * top, generator=g, device="cuda") < 0.1
+    routed = int((~lost).sum())
+    there = slots[~lost][torch.randperm(routed, generator=g, device="cuda")]
+    places = torch.full((T * top,), -1, dtype=torch.int32, device="cuda")
+    places[there] = torch.arange(routed, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, routed], dtype=torch.int32, device="cuda")
+    dy, dw = rt().combine_rows_backward(dout, y, w, places.view(T, top), off)
+    steps = 8 * -(-N // 2048) + 10
+    # tokens' slots in the order of y's rows, a few thousand at a time
+    assert bool((dw.reshape(-1)[lost] == 0).all()) and bool((dy[routed:] == 0).all())
+    for first in range(0, routed, 4096):
+        at = there[first:first + 4096]
+        d, x = dout[at // top].double(), y[first:first + at.numel()].double()
+        prod, scale = d * x, w.reshape(-1)[at].double()[:, None]
+        assert bool(((dw.reshape(-1)[at].double() - prod.sum(1)).abs()
+                     <= steps * U * prod.abs().sum(1) + 2.0 ** -126).all())
+        want = d * scale
+        assert bool(((dy[first:first + at.numel()].double() - want).abs()
+                     <= (HALF[dtype] * (1 + U) + U) * want.abs() + TINY[dtype]).all())
+
+
+@pytest.mark.parametrize("N", [8, 5, 2056])
+def test_combine_of_more_tokens_than_one_launch_takes(N):
+    """A launch takes 2^22 workgroups: 2^22 tokens, half as many of more than 2048 columns.
+    Whole numbers, so that every step is exact."""
+    T = (1 << 22) + 5 if N < 100 else (1 << 21) + 5
+    say(f"combine of {T} tokens of {N}")
+    t = torch.arange(T, device="cuda")
+    n = torch.arange(N, device="cuda")
+    y = (((t % 61).to(torch.int16)[:, None] + (n % 61).to(torch.int16)) % 61).to(torch.bfloat16)
+    places = (T - 1 - t).to(torch.int32)[:, None].contiguous()
+    w = (t % 3).float()[:, None]
+    out = rt().combine_rows(y, w, places)
+    assert torch.equal(out, y.flip(0) * w.to(torch.bfloat16))
+    if N > 100:
+        return
+    off = torch.tensor([T - 2], dtype=torch.int32, device="cuda")
+    dy, dw = rt().combine_rows_backward(y, y, w, places, off)
+    want = (y * w.to(torch.bfloat16)).flip(0)          # row T - 1 - t is w[t] y[t]
+    want[T - 2:] = 0
+    assert torch.equal(dy, want)
+    dots = (y.float() * y.flip(0).float()).sum(1)
+    dots[:2] = 0                                       # places T - 1 and T - 2
+    assert torch.equal(dw[:, 0], dots)
