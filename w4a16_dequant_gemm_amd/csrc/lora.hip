@@ -902,26 +902,38 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
             base[j] = (const uint16_t*)args.base + row * args.ldb;
             out[j] = (uint16_t*)args.out + row * args.ldo;
         }
+        f32x4 h[KH][2];
         u32x4 part[KH][kParts];
         float back[4] = {1.0f, 1.0f, 1.0f, 1.0f};
         {
             const int64_t row = min(tile0 + (tile_rows >> col & 1 ? col : one_row), args.P - 1);
-            const float* h = args.operands + row * (KH * 32) + g * 8;
+            const float* from = args.operands + row * (KH * 32) + g * 8;
 #pragma unroll
             for (int kh = 0; kh < KH; ++kh) {
-                const f32x4 p = *(const f32x4*)(h + kh * 32), q = *(const f32x4*)(h + kh * 32 + 4);
-                const float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
-                split8(v, part[kh]);
+                h[kh][0] = *(const f32x4*)(from + kh * 32);
+                h[kh][1] = *(const f32x4*)(from + kh * 32 + 4);
             }
             if constexpr (!BF16)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     back[j] = args.back[min(tile0 + (mine[j] ? g * 4 + j : one_row), args.P - 1)];
         }
+        // Not before the first loads of the adapter and of base are issued, which would wait for
+        // h (4096 rows K = 8192, N = 28672, R = 64: 143 -> 139 us a call); the empty asm keeps
+        // its steps from being taken out of the two ways that have them.
+        auto split_h = [&]() {
+#pragma unroll
+            for (int kh = 0; kh < KH; ++kh) {
+                asm volatile("" : "+v"(h[kh][0]), "+v"(h[kh][1]));
+                const f32x4 p = h[kh][0], q = h[kh][1];
+                const float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+                split8(v, part[kh]);
+            }
+        };
         // operands of the adapter a few at a time, each part of h with all of them: products that
-        // follow one another do not wait for each other's sums (bf16's third part costs 4096
-        // rows R = 128 nothing, 222 -> 218 us; one after the other 239).  Up to 3 operands
-        // 4 at a time would cost waves.
+        // follow one another do not wait for each other's sums (4096 rows R = 128: 239 -> 216 us
+        // a call; bf16's third part costs nothing so).  Up to 3 operands 4 at a time would
+        // cost waves.
         auto multiply = [&](f32x4 (&d)[8], const uint8_t* my_ranks) {
             constexpr int kAtOnce = KH <= 3 ? 2 : 4;
 #pragma unroll
@@ -963,6 +975,7 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
                 load_base_run(y[j], first + j * kWideCols);
                 __builtin_amdgcn_sched_barrier(0);   // in the order of the loop
             }
+            split_h();
             // whole rounds of the ring (a way from its first stage to itself would make that
             // wait for the others' loads)
             for (int64_t n0 = first; n0 < whole;) {
@@ -984,6 +997,8 @@ __global__ __launch_bounds__(256, KH <= 3 ? 2 : 1) void up_wide_kernel(LoraArgs 
                     n0 += kWideCols;
                 }
             }
+        } else {
+            split_h();
         }
         if (whole < end) {   // N ends inside this run
             const int64_t from = max(first, whole);
