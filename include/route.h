@@ -20,8 +20,10 @@
  *
  * A NaN or +infinity among a token's logits makes its probabilities NaN: its weights,
  * the loss and its gradients show it, its experts and the order stay in range.  Logits
- * that are all -infinity give probabilities 0.  Sums are fp32 in a fixed order: equal
- * calls give equal bits.
+ * that are all -infinity give probabilities 0.  Sums are fp32 in a fixed order (that of a
+ * token's chosen probabilities, which RENORMALIZE divides by, is kept in steps of 2^-26 at
+ * most of its largest): equal calls give equal bits, and a token's experts and weights do
+ * not depend on the other tokens.
  *
  * Conventions are those of w4a16.h (plain C types, caller-owned device pointers, stream
  * as void*, asynchronous, nothing allocated, every argument validated on the host before

@@ -1,9 +1,10 @@
 """Python binding of the low-rank adapters of many requests (include/lora.h) of
 libw4a16.so.
 
-Argument marshalling only; there is no fallback.  base is what w4a16_gemm, fp8.fp8_gemm or
-another product gave for the rows x, or for the quantised rows (x, xs) of
-rowquant.rmsnorm_quantize_rows and swiglu_quantize_rows with kind "fp8".
+Argument marshalling only; there is no fallback, and no gradient: the call is not part of
+torch's autograd graph.  base is what w4a16_gemm, fp8.fp8_gemm or another product gave for
+the rows x, or for the quantised rows (x, xs) of rowquant.rmsnorm_quantize_rows and
+swiglu_quantize_rows with kind "fp8".
 """
 from __future__ import annotations
 

@@ -6,6 +6,11 @@ their gradients.
     y = fp8.fp8_grouped_gemm(q, s, packed, r.offsets, rows=r.rows)
     out = combine_rows(y, r.weights, r.places, residual=h)
 
+None of the calls is part of torch's autograd graph: what they return has no grad_fn, whether or
+not an argument requires a gradient.  A training program calls the *_backward functions itself,
+for instance from a torch.autograd.Function.  The products between the router and the sum
+have no backward here: dy is where the program's own begins.
+
 Argument marshalling only; there is no fallback.
 """
 from __future__ import annotations
