@@ -3,10 +3,11 @@
 //
 // Both are bound by HBM: every row of y is read once, nothing but the result is written
 // (bf16: 8192 tokens of 2 rows of 8192 with the residual 87 us, 6.1 TB/s; the gradient of
-// 8192 tokens of 8 rows of 4096 212 us, 5.3 TB/s; a device copy reaches 5.16).
+// 8192 tokens of 8 rows of 4096 214 us, 5.3 TB/s; a device copy reaches 5.16; medians of a trace).
 // A lane holds 8 consecutive elements of a token (one 16-byte access per row).
 // Rows may start at any element (an odd N): global memory takes 16-byte accesses at any
-// even address (the gradient of 519 tokens of 6 rows of 2831 takes 14.0 us, of 2832 13.0).
+// even address (the gradient of 519 tokens of 6 rows of 2831 takes 13.7 us back to back, of
+// 2832 12.9).
 #include <hip/hip_runtime.h>
 
 #include "route_internal.h"

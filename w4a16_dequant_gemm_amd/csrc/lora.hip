@@ -1,9 +1,9 @@
 // lora.hip -- low-rank adapters of many requests beside a shared projection
 // (include/lora.h): two products, h = x A^T (K is long, R is short) and out = base +
 // h B^T (R is short, N is long), each bound by what it reads and writes: 4096 bf16 rows of 4
-// requests, K = 8192, N = 28672, R = 64: 22 us for 67 MB of x and 90 us for 470 MB of
-// base and out (5.2 TB/s, what a copy reaches), 126-136 us with the order of the rows
-// (6) and the join of the first product's parts (5).
+// requests, K = 8192, N = 28672, R = 64: 24 us for 67 MB of x and 96 us for 470 MB of
+// base and out (4.9 TB/s; a copy reaches 5.16), 121-137 us a call with the order of the rows
+// (8) and the join of the first product's parts (5); medians of a trace.
 //
 // Rows are taken 16 at a time as columns of the matrix instruction (v_mfma_f32_16x16x32,
 // the adapter is its first operand; where there are many rows they are the first operand
@@ -88,8 +88,8 @@ __device__ __forceinline__ int row_id(const LoraArgs& a, int64_t row0, int rows,
 // group of rows may hold anything, so adapters that share a remainder only cost time).  With
 // few adapters each one's rows begin a group of their own (pad rows), the places before
 // it stay empty: no group does its work twice (4096 rows of 64 adapters at random, K =
-// 8192, N = 28672, R = 16: 204 -> 159 us).  One workgroup: 1037 rows take 3.5 us, 4096 rows
-// 5.5.
+// 8192, N = 28672, R = 16: 204 -> 159 us).  One workgroup: 1037 rows take 5.7 us, 4096 rows
+// 7.7.
 constexpr int kBins = 1024;
 
 // Adds one for every live lane to its bin; returns what the lane found there.  Lanes of one

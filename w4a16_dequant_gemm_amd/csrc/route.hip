@@ -9,9 +9,9 @@
 // the tiles' counts up, expert by expert, a third turns ranks into places (up to 1024 tokens
 // it does both); up to 64 tokens one workgroup does all of it in one launch.
 // Bound by arithmetic where there are many experts (65536 x 256 fp32 with the loss: choice
-// 30 us, of which about 18 are issued instructions and 13 would be the bytes; sums 8,
+// 32 us, of which about 18 are issued instructions and 13 would be the bytes; sums 8,
 // places 8, gradient 29 against 26 of bytes), by launches and the first loads' latency
-// elsewhere (8192 x 128 bf16: 7 + 3.5 + 4 us; 8 x 64: 4 us).
+// elsewhere (8192 x 128 bf16: 7 + 4 + 4.5 us; 8 x 64: 3.9 us; medians of a trace).
 //
 // Compiled once per type of the logits (ROUTE_TU_TYPE = 0 fp16, 1 bf16, 2 fp32).
 #include <hip/hip_runtime.h>
