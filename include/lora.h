@@ -8,7 +8,8 @@
  * base is what the shared projection (w4a16_gemm, fp8_gemm, ...) gave for x.  A row whose
  * id is outside [0, L) has no adapter: out[m] = base[m], bit for bit.  The rows of an
  * adapter may lie anywhere; what an adapter or a row holds (NaN and infinities too) is
- * seen in that adapter's or row's outputs only.  The R inner products with A are kept in
+ * seen in that adapter's or row's outputs only (an infinity in B as an infinity or a NaN,
+ * since a part of what it is multiplied by may be 0).  The R inner products with A are kept in
  * fp32; as operand of the second product each is the sum of numbers of the activations'
  * type: bf16 of three, which hold all its 24 bits, fp16 of two, which hold 22 (after a row's
  * finite ones were brought near 2^14 by a power of two).  Sums have a fixed order: equal
